@@ -44,7 +44,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     cmd = [nvcc, *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC,
-           os.path.join(CSRC, "fp8q.cu"), "-o", LIB + ".tmp"]
+           os.path.join(CSRC, "library.cu"), "-o", LIB + ".tmp"]
     proc = subprocess.run(cmd, capture_output=True, text=True)
     with open(LOG, "w") as f:
         f.write(" ".join(cmd) + "\n" + proc.stdout + proc.stderr)

@@ -1,0 +1,217 @@
+// library.cu -- the one translation unit of libfp8q.so: the quantisers and GEMMs (fp8q.cu), and the
+// C entry points of the routed expert layer's operators (kernels in moe.cuh).  One unit, so that all
+// kernels share the device status word and the launch helpers.
+#include <cmath>
+
+#include "fp8q.cu"
+
+#include "moe.cuh"
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+constexpr int64_t kI32 = 0x7FFFFFFF;
+
+// A persistent grid: `per_sm` CTAs on each SM, no more than there are work items.
+unsigned grid_for(int64_t items, int per_sm)
+{
+    int sms = sm_count();
+    if (sms <= 0) sms = 148;
+    const int64_t n = (int64_t)sms * per_sm;
+    return (unsigned)(items < n ? (items > 0 ? items : 1) : n);
+}
+
+template <typename L, bool SOFTMAX>
+int launch_route(const void* logits, const float* bias, int64_t T, int E, int k, int n_group, int topk_group,
+                 int renorm, float scale, int32_t* idx, float* w, cudaStream_t st)
+{
+    const dim3 grid((unsigned)((T + 3) / 4));
+    const L* l = static_cast<const L*>(logits);
+#define FP8Q_ROUTE(NV)                                                                                              \
+    return launch_kernel(moe_route_kernel<L, NV, SOFTMAX>, grid, dim3(128), 0, st, false, l, bias, T, E, k, n_group, \
+                         topk_group, renorm, scale, idx, w)
+    if (E <= 32) FP8Q_ROUTE(1);
+    if (E <= 64) FP8Q_ROUTE(2);
+    if (E <= 128) FP8Q_ROUTE(4);
+    if (E <= 256) FP8Q_ROUTE(8);
+    if (E <= 512) FP8Q_ROUTE(16);
+    FP8Q_ROUTE(32);
+#undef FP8Q_ROUTE
+}
+
+template <typename L, bool SOFTMAX>
+int launch_route_backward(const float* dw, const float* w, const int32_t* idx, const void* logits, int64_t T, int E,
+                          int k, int renorm, float scale, void* dlogits, cudaStream_t st)
+{
+    const dim3 grid((unsigned)((T + 3) / 4));
+    const L* l = static_cast<const L*>(logits);
+    L* d = static_cast<L*>(dlogits);
+#define FP8Q_ROUTE(NV)                                                                                              \
+    return launch_kernel(moe_route_backward_kernel<L, NV, SOFTMAX>, grid, dim3(128), 0, st, false, dw, w, idx, l, T, \
+                         E, k, renorm, scale, d)
+    if (E <= 32) FP8Q_ROUTE(1);
+    if (E <= 64) FP8Q_ROUTE(2);
+    if (E <= 128) FP8Q_ROUTE(4);
+    if (E <= 256) FP8Q_ROUTE(8);
+    if (E <= 512) FP8Q_ROUTE(16);
+    FP8Q_ROUTE(32);
+#undef FP8Q_ROUTE
+}
+
+// What both directions of the router ask of their scalar arguments.
+int route_args(int logits_type, int64_t T, int32_t E, int32_t k, int score, float scale)
+{
+    if (T < 0 || E < 1 || k < 1 || k > E) return FP8Q_ERR_ARG;
+    if (logits_type != FP8Q_LOGITS_FP32 && logits_type != FP8Q_LOGITS_BF16) return FP8Q_ERR_ARG;
+    if (score != FP8Q_SCORE_SIGMOID && score != FP8Q_SCORE_SOFTMAX) return FP8Q_ERR_ARG;
+    if (!std::isfinite(scale) || scale == 0.0f) return FP8Q_ERR_ARG;
+    if (E > kMoeMaxExperts || k > kMoeMaxTopK || T > kI32 / k) return FP8Q_ERR_UNSUPPORTED;
+    return FP8Q_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8q_moe_route(const void* logits, int logits_type, const float* bias, int64_t T, int32_t E, int32_t k,
+                   int32_t n_group, int32_t topk_group, int score, int renormalize, float scale, int32_t* idx,
+                   float* w, fp8q_stream_t stream)
+{
+    const int rc = route_args(logits_type, T, E, k, score, scale);
+    if (rc != FP8Q_OK) return rc;
+    if (n_group < 1 || topk_group < 1 || topk_group > n_group || E % n_group != 0) return FP8Q_ERR_ARG;
+    if ((int64_t)topk_group * (E / n_group) < k) return FP8Q_ERR_ARG;
+    if (n_group > kMoeMaxGroups) return FP8Q_ERR_UNSUPPORTED;
+    if (T == 0) return FP8Q_OK;
+    if (!logits || !idx || !w) return FP8Q_ERR_ARG;
+    const bool bf16 = logits_type == FP8Q_LOGITS_BF16;
+    if ((reinterpret_cast<uintptr_t>(logits) & (bf16 ? 1u : 3u)) != 0 || !aligned4(bias) || !aligned4(idx) ||
+        !aligned4(w))
+        return FP8Q_ERR_ALIGN;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const bool softmax = score == FP8Q_SCORE_SOFTMAX;
+    const auto launch = bf16 ? (softmax ? launch_route<uint16_t, true> : launch_route<uint16_t, false>)
+                             : (softmax ? launch_route<float, true> : launch_route<float, false>);
+    return launch(logits, bias, T, E, k, n_group, topk_group, renormalize != 0, scale, idx, w, st);
+}
+
+int fp8q_moe_route_backward(const float* dw, const float* w, const int32_t* idx, const void* logits, int logits_type,
+                            int64_t T, int32_t E, int32_t k, int score, int renormalize, float scale, void* dlogits,
+                            fp8q_stream_t stream)
+{
+    const int rc = route_args(logits_type, T, E, k, score, scale);
+    if (rc != FP8Q_OK) return rc;
+    if (T == 0) return FP8Q_OK;
+    if (!dw || !w || !idx || !logits || !dlogits) return FP8Q_ERR_ARG;
+    const bool bf16 = logits_type == FP8Q_LOGITS_BF16;
+    const uintptr_t both = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits);
+    if ((both & (bf16 ? 1u : 3u)) != 0 || !aligned4(dw) || !aligned4(w) || !aligned4(idx)) return FP8Q_ERR_ALIGN;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const bool softmax = score == FP8Q_SCORE_SOFTMAX;
+    const auto launch =
+        bf16 ? (softmax ? launch_route_backward<uint16_t, true> : launch_route_backward<uint16_t, false>)
+             : (softmax ? launch_route_backward<float, true> : launch_route_backward<float, false>);
+    return launch(dw, w, idx, logits, T, E, k, renormalize != 0, scale, dlogits, st);
+}
+
+int fp8q_moe_plan(const int32_t* idx, int64_t T, int32_t k, int32_t E, int32_t* offsets, int32_t* slots,
+                  int32_t* rows, fp8q_stream_t stream)
+{
+    if (T < 0 || k < 1 || E < 1) return FP8Q_ERR_ARG;
+    if (E > kMoeMaxExperts || k > kMoeMaxTopK || T > kI32 / k) return FP8Q_ERR_UNSUPPORTED;
+    if (!offsets || (T > 0 && (!idx || !slots || !rows))) return FP8Q_ERR_ARG;
+    if (!aligned4(idx) || !aligned4(offsets) || !aligned4(slots) || !aligned4(rows)) return FP8Q_ERR_ALIGN;
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (T == 0) {
+        const size_t bytes = (size_t)(E + 1) * sizeof(int32_t);
+        return cudaMemsetAsync(offsets, 0, bytes, st) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+    }
+    const size_t smem = (size_t)E * kPlanWarps * sizeof(int32_t);
+    if (cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMoeMaxExperts * kPlanWarps * (int)sizeof(int32_t)) != cudaSuccess)
+        return FP8Q_ERR_CUDA;
+    return launch_kernel(moe_plan_kernel, dim3(1), dim3(kPlanThreads), smem, st, false, idx, T * k, (int)E, offsets,
+                         slots, rows);
+}
+
+int fp8q_moe_dispatch(const uint16_t* x, const int32_t* offsets, const int32_t* slots, const int32_t* rows,
+                      const float* weights, int32_t E, int64_t T, int32_t k, int64_t C, uint8_t* q, float* s,
+                      uint8_t* qt, float* st, int64_t Kcap, fp8q_stream_t stream)
+{
+    if (T < 0 || k < 1 || E < 1 || C < 0 || Kcap < 0) return FP8Q_ERR_ARG;
+    if (E > kMoeMaxExperts || k > kMoeMaxTopK || T > kI32 / k || C > kI32 || Kcap > kI32) return FP8Q_ERR_UNSUPPORTED;
+    if (C % 128 != 0 || Kcap % 128 != 0) return FP8Q_ERR_SHAPE;
+    if (T == 0 || C == 0) return FP8Q_OK;
+    if (!x || !offsets || !slots || !rows || !q || !s || (qt == nullptr) != (st == nullptr)) return FP8Q_ERR_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(s) || !aligned16(qt) || !aligned16(st)) return FP8Q_ERR_ALIGN;
+    if (!aligned4(offsets) || !aligned4(slots) || !aligned4(rows) || !aligned4(weights)) return FP8Q_ERR_ALIGN;
+    const cudaStream_t cs = (cudaStream_t)stream;
+    const int64_t M = T * k;
+    if (!qt)
+        return launch_kernel(moe_dispatch_rows_kernel, dim3(grid_for((M * (C / 128) + 31) / 32, 8)), dim3(256), 0, cs,
+                             false, x, rows, weights, T, (int)k, (int)C, q, s);
+    const int64_t tiles = ((M + 127) / 128 + E) * (C / 128);
+    return launch_kernel(moe_dispatch_both_kernel, dim3(grid_for(tiles, 2)), dim3(256), 0, cs, false, x, slots,
+                         weights, offsets, (int)E, M, (int)k, C, q, s, qt, st, Kcap);
+}
+
+int fp8q_moe_combine(const uint16_t* y, const int32_t* rows, const float* weights, const uint16_t* add, int64_t T,
+                     int32_t k, int64_t C, uint16_t* out, fp8q_stream_t stream)
+{
+    if (T < 0 || k < 1 || C < 0) return FP8Q_ERR_ARG;
+    if (k > kMoeMaxTopK || T > kI32 / k || C > kI32) return FP8Q_ERR_UNSUPPORTED;
+    if (C % 8 != 0) return FP8Q_ERR_SHAPE;
+    if (T == 0 || C == 0) return FP8Q_OK;
+    if (!y || !rows || !out) return FP8Q_ERR_ARG;
+    if (!aligned16(y) || !aligned16(add) || !aligned16(out) || !aligned4(rows) || !aligned4(weights))
+        return FP8Q_ERR_ALIGN;
+    return launch_kernel(moe_combine_kernel, dim3(grid_for((T * (C / 8) + 255) / 256, 8)), dim3(256), 0,
+                         (cudaStream_t)stream, false, y, rows, weights, add, T, (int)k, C, out);
+}
+
+int fp8q_moe_combine_dweight(const uint16_t* dout, const uint16_t* y, const int32_t* rows, int64_t T, int32_t k,
+                             int64_t C, float* dw, fp8q_stream_t stream)
+{
+    if (T < 0 || k < 1 || C < 0) return FP8Q_ERR_ARG;
+    if (k > kMoeMaxTopK || T > kI32 / k || C > kI32) return FP8Q_ERR_UNSUPPORTED;
+    if (C % 8 != 0) return FP8Q_ERR_SHAPE;
+    if (T == 0) return FP8Q_OK;
+    if (!dw || !rows || (C > 0 && (!dout || !y))) return FP8Q_ERR_ARG;
+    if (!aligned16(dout) || !aligned16(y) || !aligned4(rows) || !aligned4(dw)) return FP8Q_ERR_ALIGN;
+    return launch_kernel(moe_combine_dweight_kernel, dim3((unsigned)((T * k + 7) / 8)), dim3(256), 0,
+                         (cudaStream_t)stream, false, dout, y, rows, T, (int)k, C, dw);
+}
+
+int fp8q_swiglu_quant(const uint16_t* h, int64_t M, int64_t I, uint8_t* q, float* s, uint8_t* hq, float* hs,
+                      fp8q_stream_t stream)
+{
+    if (M < 0 || I < 0) return FP8Q_ERR_ARG;
+    if (I % 128 != 0) return FP8Q_ERR_SHAPE;
+    if (M == 0 || I == 0) return FP8Q_OK;
+    if (M > kI32 || I > kI32 / 2) return FP8Q_ERR_UNSUPPORTED;
+    if (!h || !q || !s || (hq == nullptr) != (hs == nullptr)) return FP8Q_ERR_ARG;
+    if (!aligned16(h) || !aligned16(q) || !aligned16(s) || !aligned16(hq) || !aligned16(hs)) return FP8Q_ERR_ALIGN;
+    return launch_kernel(swiglu_quant_kernel, dim3(grid_for((M * (I / 128) + 31) / 32, 8)), dim3(256), 0,
+                         (cudaStream_t)stream, false, h, M, I, q, s, hq, hs);
+}
+
+int fp8q_swiglu_backward_quant(const uint16_t* da, const uint8_t* hq, const float* hs, const int32_t* offsets,
+                               int32_t E, int64_t M, int64_t I, uint8_t* q, float* s, uint8_t* qt, float* st,
+                               uint8_t* aqt, float* ast, int64_t Kcap, fp8q_stream_t stream)
+{
+    if (M < 0 || I < 0 || E < 1 || Kcap < 0 || (!offsets && E != 1)) return FP8Q_ERR_ARG;
+    if (I % 128 != 0 || Kcap % 128 != 0) return FP8Q_ERR_SHAPE;
+    if (E > kMoeMaxExperts || M > kI32 || I > kI32 / 2 || Kcap > kI32) return FP8Q_ERR_UNSUPPORTED;
+    if (M == 0 || I == 0) return FP8Q_OK;
+    if (!da || !hq || !hs || !q || !s || !qt || !st || !aqt || !ast) return FP8Q_ERR_ARG;
+    if (!offsets && Kcap < M) return FP8Q_ERR_SHAPE;
+    if (!aligned16(da) || !aligned16(hq) || !aligned16(hs) || !aligned16(q) || !aligned16(s) || !aligned16(qt) ||
+        !aligned16(st) || !aligned16(aqt) || !aligned16(ast) || !aligned4(offsets))
+        return FP8Q_ERR_ALIGN;
+    const int64_t tiles = ((M + 127) / 128 + E) * (I / 128);
+    return launch_kernel(swiglu_backward_kernel, dim3(grid_for(tiles, 2)), dim3(256), 0, (cudaStream_t)stream, false,
+                         da, hq, hs, offsets, (int)E, M, I, q, s, qt, st, aqt, ast, Kcap);
+}
+
+}  // extern "C"

@@ -1,0 +1,850 @@
+// moe.cuh -- the operators of a routed expert layer around the grouped GEMMs: routing, the expert
+// order of the rows (plan), dispatch into quantised rows, combine back to tokens, and the SwiGLU
+// between the experts' two GEMMs with its 8-bit checkpoint.  Everything here streams through HBM
+// (routing and the plan excepted: their data is small and latency counts), so the design rule is
+// one pass: quantised outputs leave from registers, gathers replace copies.
+#pragma once
+
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "ptx.cuh"
+#include "quant.cuh"
+
+namespace fp8q {
+
+constexpr int kDevBadOffsets = 2;   // FP8Q_DEV_BAD_OFFSETS
+constexpr int kDevBadIndex = 4;     // FP8Q_DEV_BAD_INDEX
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxTopK = 32;
+constexpr int kMoeMaxGroups = 32;
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+__device__ __forceinline__ float load_logit(const float* p) { return *p; }
+__device__ __forceinline__ float load_logit(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+
+__device__ __forceinline__ uint32_t bf16_rn(float x)
+{
+    uint16_t r;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = (uint16_t)bf16_rn(v); }
+
+// ------------------------------------------------------------------------------------------
+// Routing.  One warp per token; lane l holds experts l, l + 32, ...  The order of the experts is
+// that of key = score + bias in binary64 (without a bias that of the logits themselves, which is
+// the same order and needs no arithmetic); equal keys go to the lower index.  A masked expert
+// (logit or bias -inf, NaN or +inf) has the key -inf.
+// ------------------------------------------------------------------------------------------
+struct Ranked {
+    double key;
+    int e;
+};
+__device__ __forceinline__ bool before(double ka, int ea, double kb, int eb)
+{
+    return ka > kb || (ka == kb && ea < eb);
+}
+__device__ __forceinline__ Ranked warp_first(Ranked r)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        const double k = __shfl_xor_sync(kFull, r.key, o);
+        const int e = __shfl_xor_sync(kFull, r.e, o);
+        if (before(k, e, r.key, r.e)) {
+            r.key = k;
+            r.e = e;
+        }
+    }
+    return r;
+}
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ T warp_sum(T v)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+template <typename L, int NV, bool SOFTMAX>
+__global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ logits, const float* __restrict__ bias,
+                                                        int64_t T, int E, int k, int n_group, int topk_group,
+                                                        int renorm, float scale, int32_t* __restrict__ idx,
+                                                        float* __restrict__ w)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (t >= T) return;
+    const L* row = logits + t * E;
+    const int per = E / n_group;
+
+    float l[NV];
+    bool bad = false;
+    float top = -CUDART_INF_F;   // the largest usable logit
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane + 32 * i;
+        l[i] = -CUDART_INF_F;
+        if (e < E) {
+            const float x = load_logit(row + e);
+            const float b = bias ? bias[e] : 0.0f;
+            bad |= !(x < CUDART_INF_F) || !(b < CUDART_INF_F);
+            if (x < CUDART_INF_F) l[i] = x;
+        }
+        top = fmaxf(top, l[i]);
+    }
+    bad = __any_sync(kFull, bad);
+    top = warp_max(top);
+    double total = 1.0;
+    if (SOFTMAX) {
+        total = 0.0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (l[i] > -CUDART_INF_F) total += exp((double)l[i] - (double)top);
+        total = warp_sum(total);
+    }
+
+    double key[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane + 32 * i;
+        key[i] = -CUDART_INF;
+        if (e < E && l[i] > -CUDART_INF_F) {
+            if (bias) {
+                const float b = bias[e];
+                const double s = SOFTMAX ? exp((double)l[i] - (double)top) / total : 1.0 / (1.0 + exp(-(double)l[i]));
+                if (b > -CUDART_INF_F && b < CUDART_INF_F) key[i] = s + (double)b;
+            } else {
+                key[i] = (double)l[i];
+            }
+        }
+    }
+
+    uint32_t allowed = kFull;   // bit g: experts of group g may be chosen
+    if (n_group > 1) {
+        double mine = -CUDART_INF;   // lane g: the score of group g
+        for (int g = 0; g < n_group; ++g) {
+            Ranked r1{-CUDART_INF, 0x7FFFFFFF}, r2{-CUDART_INF, 0x7FFFFFFF};
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = lane + 32 * i;
+                if (e / per == g && before(key[i], e, r1.key, r1.e)) r1 = Ranked{key[i], e};
+            }
+            r1 = warp_first(r1);
+            double score = r1.key;
+            if (bias) {   // the sum of the two largest keys (of the one there is)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int e = lane + 32 * i;
+                    if (e / per == g && e != r1.e && before(key[i], e, r2.key, r2.e)) r2 = Ranked{key[i], e};
+                }
+                r2 = warp_first(r2);
+                if (r2.key > -CUDART_INF) score += r2.key;
+            }
+            if (lane == g) mine = score;
+        }
+        int rank = 0;
+        for (int g = 0; g < n_group; ++g) {
+            const double other = __shfl_sync(kFull, mine, g);
+            if (before(other, g, mine, lane)) ++rank;
+        }
+        allowed = __ballot_sync(kFull, lane < n_group && rank < topk_group);
+    }
+
+    uint32_t taken = 0u;
+    int chosen = 0;   // lane j: the j-th expert
+    for (int j = 0; j < k; ++j) {
+        Ranked r{-CUDART_INF, 0x7FFFFFFF};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = lane + 32 * i;
+            if (e < E && !((taken >> i) & 1u) && ((allowed >> (e / per)) & 1u) && before(key[i], e, r.key, r.e))
+                r = Ranked{key[i], e};
+        }
+        r = warp_first(r);
+        if ((r.e & 31) == lane) taken |= 1u << (r.e >> 5);
+        if (lane == j) chosen = r.e;
+    }
+
+    // Weights.  The renormalised ones divide scores by their sum, so scores that would underflow are
+    // first scaled by exp(-m), m = min(largest chosen logit, 0): sigmoid(l) e^-m = e^(l-m) / (1 + e^l).
+    bool usable = false;
+    float x = -CUDART_INF_F;
+    if (lane < k) {
+        x = load_logit(row + chosen);
+        const float b = bias ? bias[chosen] : 0.0f;
+        usable = x > -CUDART_INF_F && x < CUDART_INF_F && b > -CUDART_INF_F && b < CUDART_INF_F;
+    }
+    const float best = warp_max(usable ? x : -CUDART_INF_F);
+    double s = 0.0;
+    if (usable) {
+        const double m = renorm ? (SOFTMAX ? (double)best : fmin((double)best, 0.0)) : 0.0;
+        if (SOFTMAX)
+            s = renorm ? exp((double)x - m) : exp((double)x - (double)top) / total;
+        else
+            s = x > 0.0f ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - m) / (1.0 + exp((double)x));
+    }
+    if (renorm) {
+        const double sum = warp_sum(s);
+        s = sum > 0.0 ? s / sum : 0.0;
+    }
+    if (lane < k) {
+        idx[t * k + lane] = chosen;
+        w[t * k + lane] = bad ? CUDART_NAN_F : (float)(s * (double)scale);
+    }
+}
+
+// Gradient of the weights with respect to the logits, g = dL/dw, p_j = w_j / scale:
+//   renormalised:  sigmoid  dl_j = w_j (1 - s_j) sum_i p_i (g_j - g_i)     softmax the same without (1 - s_j)
+//   as they are:   sigmoid  dl_j = w_j (1 - s_j) g_j                       softmax dl_e = [chosen] w_e g_e - p_e sum_i w_i g_i
+// (sum_i p_i = 1 turns g_j - sum_i p_i g_i into differences, which do not cancel.)  A slot of
+// weight zero takes no part; every other expert's gradient is zero and is written.
+template <typename L, int NV, bool SOFTMAX>
+__global__ void __launch_bounds__(128) moe_route_backward_kernel(const float* __restrict__ dw,
+                                                                 const float* __restrict__ w,
+                                                                 const int32_t* __restrict__ idx,
+                                                                 const L* __restrict__ logits, int64_t T, int E,
+                                                                 int k, int renorm, float scale,
+                                                                 L* __restrict__ dlogits)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (t >= T) return;
+    const L* row = logits + t * E;
+    int e = -1;
+    float g = 0.0f, wt = 0.0f;
+    if (lane < k) {
+        e = idx[t * k + lane];
+        wt = w[t * k + lane];
+        g = dw[t * k + lane];
+        if (e < 0 || e >= E) {
+            latch_status(kDevBadIndex);
+            e = -1;
+        }
+    }
+    const bool live = e >= 0 && wt != 0.0f;
+    const float p = live ? wt / scale : 0.0f;
+    if (!live) g = 0.0f;
+    float d = 0.0f;
+    if (renorm) {
+        for (int i = 0; i < k; ++i) d += __shfl_sync(kFull, p, i) * (g - __shfl_sync(kFull, g, i));
+    } else {
+        d = g;
+    }
+    if (!SOFTMAX && live) {
+        const float x = load_logit(row + e);
+        d *= 1.0f / (1.0f + expf(x));   // 1 - sigmoid(x)
+    }
+    d = live ? d * wt : 0.0f;
+
+    float sum = 0.0f, top = -CUDART_INF_F, inv = 0.0f;
+    float l[NV];
+    const bool dense = SOFTMAX && !renorm;
+    if (dense) {
+        sum = warp_sum(d);
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = lane + 32 * i;
+            l[i] = -CUDART_INF_F;
+            if (c < E) {
+                const float x = load_logit(row + c);
+                if (x < CUDART_INF_F) l[i] = x;
+            }
+            top = fmaxf(top, l[i]);
+        }
+        top = warp_max(top);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) total += l[i] > -CUDART_INF_F ? expf(l[i] - top) : 0.0f;
+        total = warp_sum(total);
+        inv = total > 0.0f ? 1.0f / total : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = lane + 32 * i;
+        float v = 0.0f;
+        if (dense && l[i] > -CUDART_INF_F) v = -sum * (expf(l[i] - top) * inv);
+        for (int j = 0; j < k; ++j) {
+            const int ej = __shfl_sync(kFull, e, j);
+            const float dj = __shfl_sync(kFull, d, j);
+            if (ej == c) v += dj;
+        }
+        if (c < E) store_logit(dlogits + t * E + c, v);
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// The plan: a stable counting sort of the M = T k slots by expert.  One CTA; warp w owns a
+// contiguous run of slots and counts its experts 32 at a time (match.any finds a slot's rank among
+// the 32), the counts are scanned over (expert, warp), and a second walk over the same slots places
+// them.  No atomics, so the order is a function of the input alone.
+// ------------------------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+__global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const int32_t* __restrict__ idx, int64_t M, int E,
+                                                                int32_t* __restrict__ offsets,
+                                                                int32_t* __restrict__ slots,
+                                                                int32_t* __restrict__ rows)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    extern __shared__ int32_t counts[];   // [E][kPlanWarps]
+    __shared__ int32_t part[kPlanWarps];
+    __shared__ int s_bad;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < E * kPlanWarps; i += kPlanThreads) counts[i] = 0;
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    const int64_t run = ((M + kPlanThreads - 1) / kPlanThreads) * 32;
+    const int64_t lo = min(M, run * w), hi = min(M, lo + run);
+    bool bad = false;
+    for (int64_t b = lo; b < hi; b += 32) {
+        const int64_t i = b + lane;
+        int e = i < hi ? idx[i] : -1;
+        if (i < hi && (e < 0 || e >= E)) bad = true;
+        if (e < 0 || e >= E) e = -1;
+        const unsigned peers = __match_any_sync(kFull, e);
+        if (e >= 0 && lane == __ffs(peers) - 1) counts[e * kPlanWarps + w] += __popc(peers);
+        __syncwarp();
+    }
+    if (bad) s_bad = 1;
+    __syncthreads();
+    if (s_bad) {   // an expert outside [0, E): an empty plan, which every reader refuses
+        if (tid == 0) latch_status(kDevBadIndex);
+        for (int i = tid; i <= E; i += kPlanThreads) offsets[i] = 0;
+        for (int64_t i = tid; i < M; i += kPlanThreads) {
+            slots[i] = -1;
+            rows[i] = -1;
+        }
+        return;
+    }
+    // Exclusive scan of the E x 32 counts in order: each thread a run of them, then the runs.
+    const int n = E * kPlanWarps;
+    const int each = (n + kPlanThreads - 1) / kPlanThreads;
+    const int a = min(n, tid * each), z = min(n, a + each);
+    int32_t local = 0;
+    for (int i = a; i < z; ++i) local += counts[i];
+    int32_t incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) part[w] = incl;
+    __syncthreads();
+    if (w == 0) {
+        int32_t v = part[lane], c = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(kFull, c, o);
+            if (lane >= o) c += y;
+        }
+        part[lane] = c - v;
+    }
+    __syncthreads();
+    int32_t at = part[w] + incl - local;
+    for (int i = a; i < z; ++i) {
+        const int32_t c = counts[i];
+        counts[i] = at;
+        if ((i & (kPlanWarps - 1)) == 0) offsets[i / kPlanWarps] = at;
+        at += c;
+    }
+    if (tid == 0) offsets[E] = (int32_t)M;
+    __syncthreads();
+    for (int64_t b = lo; b < hi; b += 32) {
+        const int64_t i = b + lane;
+        const int e = i < hi ? idx[i] : -1;
+        const unsigned peers = __match_any_sync(kFull, e);
+        int32_t base = 0;
+        if (e >= 0) base = counts[e * kPlanWarps + w];
+        __syncwarp();
+        if (e >= 0) {
+            const int32_t r = base + __popc(peers & ((1u << lane) - 1u));
+            slots[r] = (int32_t)i;
+            rows[i] = r;
+            if (lane == __ffs(peers) - 1) counts[e * kPlanWarps + w] = base + __popc(peers);
+        }
+        __syncwarp();
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// Dispatch, 1x128 codes only: v[r] = (weight of slot) * x[slot / k], quantised where it lands.
+// Eight lanes own one 128-element tile of one slot.
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&f)[16])
+{
+    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        f[2 * i] = bf16_lo(u[i]);
+        f[2 * i + 1] = bf16_hi(u[i]);
+    }
+}
+__device__ __forceinline__ float amax16f(const float (&f)[16])
+{
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
+    return m;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float inv)
+{
+    return e4m3x2(__fmul_rn(a, inv), __fmul_rn(b, inv)) | (e4m3x2(__fmul_rn(c, inv), __fmul_rn(d, inv)) << 16);
+}
+__device__ __forceinline__ uint4 quant16f(const float (&f)[16], float inv)
+{
+    return make_uint4(e4m3x4(f[0], f[1], f[2], f[3], inv), e4m3x4(f[4], f[5], f[6], f[7], inv),
+                      e4m3x4(f[8], f[9], f[10], f[11], inv), e4m3x4(f[12], f[13], f[14], f[15], inv));
+}
+// The largest of 8 neighbouring lanes (all 32 take part).
+__device__ __forceinline__ float max8(float v)
+{
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+__global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* __restrict__ x,
+                                                                const int32_t* __restrict__ rows,
+                                                                const float* __restrict__ weights, int64_t T, int k,
+                                                                int C, uint8_t* __restrict__ q,
+                                                                float* __restrict__ s)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t M = T * k;
+    const int CB = C >> 7;
+    const int64_t tiles = M * CB;
+    const int sub = threadIdx.x & 7;
+    const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 3;
+    const int64_t first = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
+    for (int64_t b = first - (first & 3); b < tiles; b += step) {   // warp-uniform: 4 tiles a warp
+        const int64_t i = b + (first & 3);
+        const bool live = i < tiles;
+        const int64_t slot = live ? i / CB : 0;
+        const int kb = live ? (int)(i - slot * CB) : 0;
+        float f[16];
+        const uint4* p = reinterpret_cast<const uint4*>(x + (slot / k) * C + kb * 128) + 2 * sub;
+        unpack16(__ldg(p), __ldg(p + 1), f);
+        if (weights) {
+            const float wt = weights[slot];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = __fmul_rn(wt, f[j]);
+        }
+        float sc, inv;
+        group_scale<false>(max8(amax16f(f)), sc, inv);
+        if (!live) continue;
+        const int32_t r = rows[slot];
+        if (r < 0 || r >= M) {
+            latch_status(kDevBadIndex);
+            continue;
+        }
+        reinterpret_cast<uint4*>(q + (int64_t)r * C + kb * 128)[sub] = quant16f(f, inv);
+        if (sub == 0) s[(int64_t)kb * M + r] = sc;
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// Tiles of 128 rows x 128 columns whose values sit in registers (warp w: rows 16w + i, lane l:
+// columns 4l + j), quantised in both directions as act_dual_tile does for bf16 inputs.
+// ------------------------------------------------------------------------------------------
+struct TileScratch {
+    float red[8][128];
+    float inv_c[128];
+    uint4 qs[128 * 8];   // transposed codes, [column][128 rows]
+};
+
+// 1x128 codes of the tile's first `nvalid` rows: to rows r0 .. of q[M, C] and s[C/128][M].
+__device__ __forceinline__ void tile_rows(const float (&v)[16][4], int nvalid, int64_t r0, int64_t c0, int64_t M,
+                                          int64_t C, uint8_t* __restrict__ q, float* __restrict__ s)
+{
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float rm[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        rm[i] = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
+    // Reduce-scatter: the maximum of row 16w + (lane >> 1) ends on lanes 2r, 2r + 1.
+#pragma unroll
+    for (int h = 8; h >= 1; h >>= 1) {
+        const bool up = lane & (2 * h);
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float send = up ? rm[i] : rm[i + h], keep = up ? rm[i + h] : rm[i];
+            rm[i] = fmaxf(keep, __shfl_xor_sync(kFull, send, 2 * h));
+        }
+    }
+    rm[0] = fmaxf(rm[0], __shfl_xor_sync(kFull, rm[0], 1));
+    float sc, inv;
+    group_scale<false>(rm[0], sc, inv);
+    const int mine = 16 * w + (lane >> 1);
+    if (!(lane & 1) && mine < nvalid) s[(c0 >> 7) * M + r0 + mine] = sc;
+    uint8_t* out = q + (r0 + 16 * w) * C + c0 + 4 * lane;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float ri = __shfl_sync(kFull, inv, 2 * i);
+        if (16 * w + i < nvalid)
+            *reinterpret_cast<uint32_t*>(out + (int64_t)i * C) = e4m3x4(v[i][0], v[i][1], v[i][2], v[i][3], ri);
+    }
+}
+
+// 128x1 codes of the whole tile (rows past its valid ones hold zeros), transposed: to columns 128 g ..
+// of qt[C, Kcap] and st[g][C].  Ends with a barrier, so the scratch can be used again.
+__device__ __forceinline__ void tile_cols(const float (&v)[16][4], int64_t g, int64_t c0, int64_t C, int64_t Kcap,
+                                          uint8_t* __restrict__ qt, float* __restrict__ st, TileScratch& sm)
+{
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float cm[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cm[j] = fmaxf(cm[j], fabsf(v[i][j]));
+    *reinterpret_cast<float4*>(&sm.red[w][4 * lane]) = make_float4(cm[0], cm[1], cm[2], cm[3]);
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        float a = sm.red[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) a = fmaxf(a, sm.red[i][threadIdx.x]);
+        float sc, inv;
+        group_scale<false>(a, sc, inv);
+        st[g * C + c0 + threadIdx.x] = sc;
+        sm.inv_c[threadIdx.x] = inv;
+    }
+    __syncthreads();
+    const float4 ic = *reinterpret_cast<const float4*>(&sm.inv_c[4 * lane]);
+    const float inv[4] = {ic.x, ic.y, ic.z, ic.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t c[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+            c[p] = e4m3x4(v[4 * p][j], v[4 * p + 1][j], v[4 * p + 2][j], v[4 * p + 3][j], inv[j]);
+        sm.qs[qt_unit<2>(4 * lane + j, w)] = make_uint4(c[0], c[1], c[2], c[3]);
+    }
+    __syncthreads();
+    qt_store_rows<2, 4>(sm.qs, 16 * w, qt, c0, Kcap, g * 128, lane);
+    __syncthreads();
+}
+
+// The padded 128-row groups of expert-ordered rows (as act_128x1_t_ragged_kernel counts them).
+struct GroupTable {
+    int off[kMoeMaxExperts + 1];
+    int pre[kMoeMaxExperts + 1];
+    int bad;
+};
+
+// Fills the table (whole CTA; `offsets` null: one sequence of M rows).  False if the offsets are
+// malformed; FP8Q_DEV_BAD_OFFSETS is then latched.
+__device__ __forceinline__ bool group_table(GroupTable& t, const int32_t* __restrict__ offsets, int E, int64_t M,
+                                            int64_t Kcap)
+{
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (w == 0) {
+        if (offsets) {
+            for (int i = lane; i <= E; i += 32) t.off[i] = __ldg(offsets + i);
+        } else if (lane < 2) {
+            t.off[lane] = lane ? (int)M : 0;
+        }
+        __syncwarp();
+        const int per = (E + 31) >> 5;
+        const int lo = min(E, lane * per), hi = min(E, lo + per);
+        int local = 0;
+        bool bad = false;
+        for (int e = lo; e < hi; ++e) {
+            const int64_t cnt = (int64_t)t.off[e + 1] - t.off[e];
+            bad |= cnt < 0 || cnt > M;
+            local += cnt > 0 && cnt <= M ? (int)((cnt + 127) >> 7) : 0;
+        }
+        int incl = local;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
+        }
+        int run = incl - local;
+        for (int e = lo; e < hi; ++e) {
+            t.pre[e] = run;
+            const int64_t cnt = (int64_t)t.off[e + 1] - t.off[e];
+            run += cnt > 0 && cnt <= M ? (int)((cnt + 127) >> 7) : 0;
+        }
+        if (lane == 31) {
+            t.pre[E] = incl;
+            bad |= t.off[0] != 0 || (int64_t)t.off[E] != M || (int64_t)incl * 128 > Kcap;
+        }
+        bad = __any_sync(kFull, bad);
+        if (lane == 0) t.bad = bad ? 1 : 0;
+    }
+    __syncthreads();
+    if (t.bad && threadIdx.x == 0) latch_status(kDevBadOffsets);
+    return !t.bad;
+}
+
+// First row and number of rows of padded group g < pre[E].
+__device__ __forceinline__ void group_rows(const GroupTable& t, int E, int g, int64_t& r0, int& nvalid)
+{
+    int lo = 0, hi = E;   // pre[lo] <= g < pre[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.pre[mid] <= g) lo = mid; else hi = mid;
+    }
+    r0 = (int64_t)t.off[lo] + 128ll * (g - t.pre[lo]);
+    nvalid = (int)min((int64_t)128, (int64_t)t.off[lo + 1] - r0);
+}
+
+// Dispatch, both forms: tiles of one padded group x 128 channels, the channel block in the outer
+// loop: at any time the whole grid gathers from a few channel blocks of x, so a token's k reads find
+// it in L2 although x as a whole need not fit.
+__global__ void __launch_bounds__(256, 2) moe_dispatch_both_kernel(
+    const uint16_t* __restrict__ x, const int32_t* __restrict__ slots, const float* __restrict__ weights,
+    const int32_t* __restrict__ offsets, int E, int64_t M, int k, int64_t C, uint8_t* __restrict__ q,
+    float* __restrict__ s, uint8_t* __restrict__ qt, float* __restrict__ st, int64_t Kcap)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    __shared__ GroupTable table;
+    __shared__ __align__(16) TileScratch sm;
+    if (!group_table(table, offsets, E, M, Kcap)) return;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t groups = table.pre[E], tiles = groups * (C >> 7);
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t cb = tile / groups;
+        const int g = (int)(tile - cb * groups);
+        int64_t r0;
+        int nvalid;
+        group_rows(table, E, g, r0, nvalid);
+        float v[16][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int n = 16 * w + i;
+            uint2 u = make_uint2(0u, 0u);
+            float wt = 1.0f;
+            if (n < nvalid) {
+                const int32_t slot = __ldg(slots + r0 + n);
+                if (slot >= 0 && slot < M) {
+                    u = __ldg(reinterpret_cast<const uint2*>(x + (int64_t)(slot / k) * C + cb * 128) + lane);
+                    if (weights) wt = __ldg(weights + slot);
+                } else if (lane == 0) {
+                    latch_status(kDevBadIndex);
+                }
+            }
+            v[i][0] = __fmul_rn(wt, bf16_lo(u.x));
+            v[i][1] = __fmul_rn(wt, bf16_hi(u.x));
+            v[i][2] = __fmul_rn(wt, bf16_lo(u.y));
+            v[i][3] = __fmul_rn(wt, bf16_hi(u.y));
+        }
+        tile_rows(v, nvalid, r0, cb * 128, M, C, q, s);
+        tile_cols(v, g, cb * 128, C, Kcap, qt, st, sm);
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// Combine: out[t] = add[t] + sum_j w[t,j] y[rows[t,j]], summed in FP32 in the order of j and rounded
+// once.  A slot of weight zero is not read.  Each thread owns 8 channels of one token.
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ void fma8(float (&acc)[8], float w, const uint4& u)
+{
+    const uint32_t p[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        acc[2 * i] = fmaf(w, bf16_lo(p[i]), acc[2 * i]);
+        acc[2 * i + 1] = fmaf(w, bf16_hi(p[i]), acc[2 * i + 1]);
+    }
+}
+
+__global__ void __launch_bounds__(256) moe_combine_kernel(const uint16_t* __restrict__ y,
+                                                          const int32_t* __restrict__ rows,
+                                                          const float* __restrict__ weights,
+                                                          const uint16_t* __restrict__ add, int64_t T, int k,
+                                                          int64_t C, uint16_t* __restrict__ out)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t units = C >> 3, M = T * k;
+    const int64_t n = T * units;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t t = i / units, u = i - t * units;
+        float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < k; ++j) {
+            const float w = weights ? __ldg(weights + t * k + j) : 1.0f;
+            const int32_t r = __ldg(rows + t * k + j);
+            if (w == 0.0f) continue;
+            if (r < 0 || r >= M) {
+                latch_status(kDevBadIndex);
+                continue;
+            }
+            fma8(acc, w, __ldg(reinterpret_cast<const uint4*>(y + (int64_t)r * C) + u));
+        }
+        if (add) fma8(acc, 1.0f, __ldg(reinterpret_cast<const uint4*>(add + t * C) + u));
+        reinterpret_cast<uint4*>(out + t * C)[u] =
+            make_uint4(bf16_rn(acc[0]) | (bf16_rn(acc[1]) << 16), bf16_rn(acc[2]) | (bf16_rn(acc[3]) << 16),
+                       bf16_rn(acc[4]) | (bf16_rn(acc[5]) << 16), bf16_rn(acc[6]) | (bf16_rn(acc[7]) << 16));
+    }
+}
+
+// dw[t,j] = <dout[t], y[rows[t,j]]>: one warp per slot, eight FP32 partial sums a lane.
+__global__ void __launch_bounds__(256) moe_combine_dweight_kernel(const uint16_t* __restrict__ dout,
+                                                                  const uint16_t* __restrict__ y,
+                                                                  const int32_t* __restrict__ rows, int64_t T, int k,
+                                                                  int64_t C, float* __restrict__ dw)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t M = T * k;
+    const int64_t slot = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    if (slot >= M) return;
+    const int32_t r = rows[slot];
+    if (r < 0 || r >= M) {
+        if (lane == 0) {
+            latch_status(kDevBadIndex);
+            dw[slot] = 0.0f;
+        }
+        return;
+    }
+    const uint4* a = reinterpret_cast<const uint4*>(dout + (slot / k) * C);
+    const uint4* b = reinterpret_cast<const uint4*>(y + (int64_t)r * C);
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t u = lane; u < (C >> 3); u += 32) {
+        const uint4 p = __ldg(a + u), z = __ldg(b + u);
+        const uint32_t pu[4] = {p.x, p.y, p.z, p.w}, zu[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            acc[2 * i] = fmaf(bf16_lo(pu[i]), bf16_lo(zu[i]), acc[2 * i]);
+            acc[2 * i + 1] = fmaf(bf16_hi(pu[i]), bf16_hi(zu[i]), acc[2 * i + 1]);
+        }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += acc[i];
+    sum = warp_sum(sum);
+    if (lane == 0) dw[slot] = sum;
+}
+
+// ------------------------------------------------------------------------------------------
+// SwiGLU: a = silu(g) u with g = h[:, :I], u = h[:, I:], quantised from FP32; with `hq`, the 1x128
+// codes of h itself are the checkpoint that the backward pass starts from.  Eight lanes own one
+// 128-element tile of a (and the two tiles of h it comes from).
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ float sigmoidf(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+__global__ void __launch_bounds__(256) swiglu_quant_kernel(const uint16_t* __restrict__ h, int64_t M, int64_t I,
+                                                           uint8_t* __restrict__ q, float* __restrict__ s,
+                                                           uint8_t* __restrict__ hq, float* __restrict__ hs)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t IB = I >> 7, tiles = M * IB;
+    const int sub = threadIdx.x & 7;
+    const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 3;
+    const int64_t first = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
+    for (int64_t b = first - (first & 3); b < tiles; b += step) {
+        const int64_t i = b + (first & 3);
+        const bool live = i < tiles;
+        const int64_t m = live ? i / IB : 0, ib = live ? i - m * IB : 0;
+        const uint4* p = reinterpret_cast<const uint4*>(h + m * 2 * I + ib * 128) + 2 * sub;
+        const uint4* pu = reinterpret_cast<const uint4*>(h + m * 2 * I + I + ib * 128) + 2 * sub;
+        float g[16], u[16], a[16];
+        unpack16(__ldg(p), __ldg(p + 1), g);
+        unpack16(__ldg(pu), __ldg(pu + 1), u);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) a[j] = g[j] * sigmoidf(g[j]) * u[j];
+        float sc, inv;
+        group_scale<false>(max8(amax16f(a)), sc, inv);
+        if (live) {
+            reinterpret_cast<uint4*>(q + m * I + ib * 128)[sub] = quant16f(a, inv);
+            if (sub == 0) s[ib * M + m] = sc;
+        }
+        if (hq) {
+            group_scale<false>(max8(amax16f(g)), sc, inv);
+            if (live) {
+                reinterpret_cast<uint4*>(hq + m * 2 * I + ib * 128)[sub] = quant16f(g, inv);
+                if (sub == 0) hs[ib * M + m] = sc;
+            }
+            group_scale<false>(max8(amax16f(u)), sc, inv);
+            if (live) {
+                reinterpret_cast<uint4*>(hq + m * 2 * I + I + ib * 128)[sub] = quant16f(u, inv);
+                if (sub == 0) hs[(IB + ib) * M + m] = sc;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void dec_e4m3x4(uint32_t w, float (&f)[4])
+{
+    uint32_t h0, h1;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"((uint16_t)(w & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"((uint16_t)(w >> 16)));
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(f[0]), "=f"(f[1]) : "r"(h0));
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(f[2]), "=f"(f[3]) : "r"(h1));
+}
+
+// SwiGLU backward from the checkpoint h^ = code * scale, r = sigmoid(g):
+//   dg = da u r (1 + g (1 - r)),   du = da g r,   a = g r u
+// Outputs: dh = [dg, du] in both forms (Dgrad's and Wgrad's operand) and a in the 128x1 form (the
+// second GEMM's Wgrad operand), so a is never kept between the passes.  One tile of 128 rows x 128
+// columns of I at a time, in three sweeps (dg, du, a) that each recompute from the tile's inputs.
+__global__ void __launch_bounds__(256, 2) swiglu_backward_kernel(
+    const uint16_t* __restrict__ da, const uint8_t* __restrict__ hq, const float* __restrict__ hs,
+    const int32_t* __restrict__ offsets, int E, int64_t M, int64_t I, uint8_t* __restrict__ q, float* __restrict__ s,
+    uint8_t* __restrict__ qt, float* __restrict__ st, uint8_t* __restrict__ aqt, float* __restrict__ ast, int64_t Kcap)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    __shared__ GroupTable table;
+    __shared__ __align__(16) TileScratch sm;
+    if (!group_table(table, offsets, E, M, Kcap)) return;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t IB = I >> 7, groups = table.pre[E], tiles = groups * IB;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int g = (int)(tile / IB);
+        const int64_t ib = tile - (int64_t)g * IB;
+        int64_t r0;
+        int nvalid;
+        group_rows(table, E, g, r0, nvalid);
+        for (int sweep = 0; sweep < 3; ++sweep) {
+            float v[16][4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int n = 16 * w + i;
+                v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.0f;
+                if (n < nvalid) {
+                    const int64_t r = r0 + n;
+                    const uint2 d = __ldg(reinterpret_cast<const uint2*>(da + r * I + ib * 128) + lane);
+                    const uint32_t gc = __ldg(reinterpret_cast<const uint32_t*>(hq + r * 2 * I + ib * 128) + lane);
+                    const uint32_t uc = __ldg(reinterpret_cast<const uint32_t*>(hq + r * 2 * I + I + ib * 128) + lane);
+                    const float gs = __ldg(hs + ib * M + r), us = __ldg(hs + (IB + ib) * M + r);
+                    float gf[4], uf[4];
+                    dec_e4m3x4(gc, gf);
+                    dec_e4m3x4(uc, uf);
+                    const float df[4] = {bf16_lo(d.x), bf16_hi(d.x), bf16_lo(d.y), bf16_hi(d.y)};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = gf[j] * gs, u = uf[j] * us, rr = sigmoidf(x), a = x * rr;
+                        v[i][j] = sweep == 0 ? df[j] * u * (rr + a * (1.0f - rr)) : sweep == 1 ? df[j] * a : a * u;
+                    }
+                }
+            }
+            const int64_t c0 = (sweep == 1 ? I : 0) + ib * 128;
+            if (sweep < 2) {
+                tile_rows(v, nvalid, r0, c0, M, 2 * I, q, s);
+                tile_cols(v, g, c0, 2 * I, Kcap, qt, st, sm);
+            } else {
+                tile_cols(v, g, c0, I, Kcap, aqt, ast, sm);
+            }
+        }
+    }
+}
+
+}  // namespace fp8q

@@ -12,15 +12,19 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8q.so")
 
 FPROP, DGRAD, WGRAD, WGRAD_ACC = 0, 1, 2, 3
-DEV_OK, DEV_TIMEOUT, DEV_BAD_OFFSETS, DEV_BAD_SCALES = 0, 1, 2, 3
+DEV_OK, DEV_TIMEOUT, DEV_BAD_OFFSETS, DEV_BAD_SCALES, DEV_BAD_INDEX = 0, 1, 2, 3, 4
 # Quantiser scale formats: the pages' max-abs scale a / 448, or the power-of-two (UE8M0) variant.
 SCALE_FORMATS = {"fp32": 0, "ue8m0": 1}
+# The router's score functions and the types its logits may have.
+SCORES = {"sigmoid": 0, "softmax": 1}
+LOGITS = {torch.float32: 0, torch.bfloat16: 1}
 
 _lib = None
 
@@ -64,6 +68,14 @@ def lib() -> ctypes.CDLL:
         "fp8q_quant_forward_fmt": [P, I64, I64, P, P, P, P, P, I64, P, P, P, I, P],
         "fp8q_weight_128x128_fmt": [P, I64, I64, P, P, P, I, P],
         "fp8_gemm_blockscaled_ue8m0": [I, P, P, P, P, P, I64, I64, I64, P, ctypes.c_size_t, P],
+        "fp8q_moe_route": [P, I, P, I64, I32, I32, I32, I32, I, I, ctypes.c_float, P, P, P],
+        "fp8q_moe_route_backward": [P, P, P, P, I, I64, I32, I32, I, I, ctypes.c_float, P, P],
+        "fp8q_moe_plan": [P, I64, I32, I32, P, P, P, P],
+        "fp8q_moe_dispatch": [P, P, P, P, P, I32, I64, I32, I64, P, P, P, P, I64, P],
+        "fp8q_moe_combine": [P, P, P, P, I64, I32, I64, P, P],
+        "fp8q_moe_combine_dweight": [P, P, P, I64, I32, I64, P, P],
+        "fp8q_swiglu_quant": [P, I64, I64, P, P, P, P, P],
+        "fp8q_swiglu_backward_quant": [P, P, P, P, I32, I64, I64, P, P, P, P, P, P, I64, P],
     }.items():
         fn = getattr(L, name)
         fn.restype = I
@@ -419,6 +431,245 @@ def grouped_gemm_blockscaled_wgrad(A: torch.Tensor, sA: torch.Tensor, B: torch.T
            lib().fp8_grouped_gemm_blockscaled_wgrad(_p(A), _p(sA), _p(B), _p(sB), _p(offsets), E, Mtot, M, N,
                                                     Kcap, _p(out), _stream(A.device)))
     return out
+
+
+# ------------------------------------------------------------------------------------------ #
+# The routed expert layer around the grouped GEMMs
+# ------------------------------------------------------------------------------------------ #
+
+class MoePlan(NamedTuple):
+    """The expert order of the T k routed rows (moe_plan): expert e's rows are offsets[e] ..
+    offsets[e+1]-1, row r holds slot slots[r] (= token * k + choice), slot (t, j) lies in rows[t, j]."""
+    offsets: torch.Tensor   # int32 [E + 1]
+    slots: torch.Tensor     # int32 [T k]
+    rows: torch.Tensor      # int32 [T, k]
+
+
+def _launch(entry: str, dev: torch.device, *args):
+    """Call an entry point with `dev` current, on its current stream, and check the status."""
+    if torch.cuda.current_device() == dev.index:
+        status = getattr(lib(), entry)(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib(), entry)(*args, _stream(dev))
+    _check(entry, status)
+
+
+def _together(dev: torch.device, *named):
+    """Every tensor of (tensor, name, ...) pairs lies on `dev`."""
+    for t, name in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _router(logits: torch.Tensor, score: str):
+    if isinstance(logits, torch.Tensor) and logits.dtype not in LOGITS:
+        raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
+    _require(logits, "logits", getattr(logits, "dtype", None), 2)
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    return LOGITS[logits.dtype], SCORES[score]
+
+
+def _plan(plan: MoePlan, dev: torch.device):
+    """Checked (T, k, E) of a plan."""
+    offsets, slots, rows = plan
+    _require(offsets, "plan.offsets", torch.int32, 1)
+    _require(slots, "plan.slots", torch.int32, 1)
+    _require(rows, "plan.rows", torch.int32, 2)
+    _together(dev, (offsets, "plan.offsets"), (slots, "plan.slots"), (rows, "plan.rows"))
+    if slots.numel() != rows.numel():
+        raise ValueError("plan.slots and plan.rows must have the same number of entries")
+    if offsets.numel() < 2:
+        raise ValueError("plan.offsets must have E+1 entries")
+    return rows.shape[0], rows.shape[1], offsets.numel() - 1
+
+
+def _weights(weights, T: int, k: int, dev: torch.device):
+    if weights is not None:
+        _require(weights, "weights", torch.float32, 2)
+        if tuple(weights.shape) != (T, k):
+            raise ValueError(f"weights must have shape {(T, k)}, got {tuple(weights.shape)}")
+        _together(dev, (weights, "weights"))
+
+
+def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None, score: str = "sigmoid",
+              n_group: int = 1, topk_group: int = 1, renormalize: bool = True, scale: float = 1.0,
+              idx: torch.Tensor | None = None, w: torch.Tensor | None = None):
+    """logits[T,E] fp32 or bf16 -> (idx[T,top_k] int32, w[T,top_k] fp32): each token's experts in
+    descending order of score + bias (ties: the lower index) among the topk_group best of n_group
+    groups, and their weights, scale * score (over the chosen scores' sum with renormalize).
+    score is "sigmoid" or "softmax"; bias[E] fp32 enters the choice only.  Masks and NaN as the header
+    says."""
+    kind, fn = _router(logits, score)
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _require(bias, "bias", torch.float32, 1)
+        if bias.numel() != E:
+            raise ValueError(f"bias must have {E} entries, got {bias.numel()}")
+    if top_k < 1:
+        raise ValueError("top_k must be at least 1")
+    idx = _out(idx, (T, top_k), torch.int32, dev, "idx")
+    w = _out(w, (T, top_k), torch.float32, dev, "w")
+    _together(dev, (bias, "bias"), (idx, "idx"), (w, "w"))
+    _launch("fp8q_moe_route", dev, _p(logits), kind, _p(bias), T, E, top_k, n_group, topk_group, fn,
+            int(renormalize), scale, _p(idx), _p(w))
+    return idx, w
+
+
+def moe_route_backward(dw: torch.Tensor, w: torch.Tensor, idx: torch.Tensor, logits: torch.Tensor,
+                       score: str = "sigmoid", renormalize: bool = True, scale: float = 1.0,
+                       out: torch.Tensor | None = None):
+    """Gradient dlogits[T,E] (the logits' type) of a loss whose gradient with respect to moe_route's w
+    is dw[T,k]; w, idx, logits, score, renormalize and scale as that call had and returned them."""
+    kind, fn = _router(logits, score)
+    T, E = logits.shape
+    dev = logits.device
+    _require(idx, "idx", torch.int32, 2)
+    k = idx.shape[1]
+    for t, name, dtype in ((dw, "dw", torch.float32), (w, "w", torch.float32), (idx, "idx", torch.int32)):
+        _require(t, name, dtype, 2)
+        if tuple(t.shape) != (T, k):
+            raise ValueError(f"{name} must have shape {(T, k)}, got {tuple(t.shape)}")
+    out = _out(out, (T, E), logits.dtype, dev, "out")
+    _together(dev, (dw, "dw"), (w, "w"), (idx, "idx"), (out, "out"))
+    _launch("fp8q_moe_route_backward", dev, _p(dw), _p(w), _p(idx), _p(logits), kind, T, E, k, fn,
+            int(renormalize), scale, _p(out))
+    return out
+
+
+def moe_plan(idx: torch.Tensor, E: int, offsets: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+             rows: torch.Tensor | None = None) -> MoePlan:
+    """idx[T,k] int32 (the experts of every token) -> the expert order of the T k rows: sorted by
+    expert, then by slot."""
+    _require(idx, "idx", torch.int32, 2)
+    T, k = idx.shape
+    dev = idx.device
+    offsets = _out(offsets, (E + 1,), torch.int32, dev, "offsets")
+    slots = _out(slots, (T * k,), torch.int32, dev, "slots")
+    rows = _out(rows, (T, k), torch.int32, dev, "rows")
+    _together(dev, (offsets, "offsets"), (slots, "slots"), (rows, "rows"))
+    _launch("fp8q_moe_plan", dev, _p(idx), T, k, E, _p(offsets), _p(slots), _p(rows))
+    return MoePlan(offsets, slots, rows)
+
+
+def moe_dispatch(x: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None = None, transposed: bool = False,
+                 Kcap: int | None = None, q: torch.Tensor | None = None, s: torch.Tensor | None = None,
+                 qt: torch.Tensor | None = None, st: torch.Tensor | None = None):
+    """x[T,C] bf16 -> (q[Tk,C], s[C/128,Tk], qt[C,Kcap] or None, st[Kcap/128,C] or None): every token's
+    row (times its slot's weight, where weights[T,k] fp32 are given) quantised in the plan's order, in
+    the 1x128 form and, with `transposed`, in the ragged 128x1 one (act_128x1_transposed_ragged's).
+    With weights this is the backward pass of moe_combine for its rows."""
+    _require(x, "x", torch.bfloat16, 2)
+    Tx, C = x.shape
+    dev = x.device
+    T, k, E = _plan(plan, dev)
+    if Tx != T:
+        raise ValueError(f"x has {Tx} tokens, the plan {T}")
+    _weights(weights, T, k, dev)
+    M = T * k
+    q = _out(q, (M, C), torch.uint8, dev, "q")
+    s = _out(s, (C // 128, M), torch.float32, dev, "s")
+    if transposed or qt is not None or st is not None:
+        Kcap = ragged_capacity(M, E) if Kcap is None else Kcap
+        qt = _out(qt, (C, Kcap), torch.uint8, dev, "qt")
+        st = _out(st, (Kcap // 128, C), torch.float32, dev, "st")
+    _together(dev, (q, "q"), (s, "s"), (qt, "qt"), (st, "st"))
+    _launch("fp8q_moe_dispatch", dev, _p(x), _p(plan.offsets), _p(plan.slots), _p(plan.rows), _p(weights), E, T, k, C,
+            _p(q), _p(s), _p(qt), _p(st), Kcap or 0)
+    return q, s, qt, st
+
+
+def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None = None,
+                add: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """y[Tk,C] bf16 rows in the plan's order -> out[T,C] bf16: add[t] + sum_j weights[t,j] y[rows[t,j]],
+    in fp32, rounded once.  Without weights it is the backward pass of moe_dispatch."""
+    _require(y, "y", torch.bfloat16, 2)
+    M, C = y.shape
+    dev = y.device
+    T, k, _ = _plan(plan, dev)
+    if M != T * k:
+        raise ValueError(f"y has {M} rows, the plan {T * k}")
+    _weights(weights, T, k, dev)
+    if add is not None:
+        add = _out(add, (T, C), torch.bfloat16, dev, "add")
+    out = _out(out, (T, C), torch.bfloat16, dev, "out")
+    _together(dev, (add, "add"), (out, "out"))
+    _launch("fp8q_moe_combine", dev, _p(y), _p(plan.rows), _p(weights), _p(add), T, k, C, _p(out))
+    return out
+
+
+def moe_combine_dweight(dout: torch.Tensor, y: torch.Tensor, plan: MoePlan, out: torch.Tensor | None = None):
+    """Gradient of moe_combine's weights: dw[T,k] fp32, dw[t,j] = <dout[t], y[rows[t,j]]>."""
+    _require(dout, "dout", torch.bfloat16, 2)
+    _require(y, "y", torch.bfloat16, 2)
+    dev = dout.device
+    T, k, _ = _plan(plan, dev)
+    C = dout.shape[1]
+    if dout.shape[0] != T or tuple(y.shape) != (T * k, C):
+        raise ValueError(f"dout must be [{T}, C] and y [{T * k}, C], got {tuple(dout.shape)} and {tuple(y.shape)}")
+    out = _out(out, (T, k), torch.float32, dev, "out")
+    _together(dev, (y, "y"), (out, "out"))
+    _launch("fp8q_moe_combine_dweight", dev, _p(dout), _p(y), _p(plan.rows), T, k, C, _p(out))
+    return out
+
+
+def swiglu_quant(h: torch.Tensor, checkpoint: bool = True, q: torch.Tensor | None = None,
+                 s: torch.Tensor | None = None, hq: torch.Tensor | None = None, hs: torch.Tensor | None = None):
+    """h[M,2I] bf16, halves [gate | up] -> (q[M,I], s[I/128,M], hq[M,2I] or None, hs[2I/128,M] or None):
+    the 1x128 codes of silu(gate) * up for the next GEMM, and with `checkpoint` those of h, which is
+    all that swiglu_backward_quant needs."""
+    _require(h, "h", torch.bfloat16, 2)
+    M, two = h.shape
+    dev = h.device
+    if two % 2:
+        raise ValueError(f"h must have an even number of columns, got {two}")
+    I = two // 2
+    q = _out(q, (M, I), torch.uint8, dev, "q")
+    s = _out(s, (I // 128, M), torch.float32, dev, "s")
+    if checkpoint or hq is not None or hs is not None:
+        hq = _out(hq, (M, two), torch.uint8, dev, "hq")
+        hs = _out(hs, (two // 128, M), torch.float32, dev, "hs")
+    _together(dev, (q, "q"), (s, "s"), (hq, "hq"), (hs, "hs"))
+    _launch("fp8q_swiglu_quant", dev, _p(h), M, I, _p(q), _p(s), _p(hq), _p(hs))
+    return q, s, hq, hs
+
+
+def swiglu_backward_quant(da: torch.Tensor, hq: torch.Tensor, hs: torch.Tensor, offsets: torch.Tensor | None = None,
+                          Kcap: int | None = None, q: torch.Tensor | None = None, s: torch.Tensor | None = None,
+                          qt: torch.Tensor | None = None, st: torch.Tensor | None = None,
+                          aqt: torch.Tensor | None = None, ast: torch.Tensor | None = None):
+    """da[M,I] bf16 and the checkpoint (hq, hs) of swiglu_quant -> (q[M,2I], s[2I/128,M], qt[2I,Kcap],
+    st[Kcap/128,2I], aqt[I,Kcap], ast[Kcap/128,I]): the gradient of h in both operand forms, and the
+    recomputed silu(gate) * up in the 128x1 form.  offsets int32[E+1] on the device group the rows by
+    expert (as act_128x1_transposed_ragged); without them they are one sequence, padded to Kcap =
+    the next multiple of 128."""
+    _require(da, "da", torch.bfloat16, 2)
+    _require(hq, "hq", torch.uint8, 2)
+    _require(hs, "hs", torch.float32, 2)
+    M, I = da.shape
+    dev = da.device
+    if tuple(hq.shape) != (M, 2 * I) or tuple(hs.shape) != (2 * I // 128, M):
+        raise ValueError(f"the checkpoint of [{M}, {2 * I}] has codes {(M, 2 * I)} and scales {(2 * I // 128, M)}, "
+                         f"got {tuple(hq.shape)} and {tuple(hs.shape)}")
+    E = 1
+    if offsets is not None:
+        _require(offsets, "offsets", torch.int32, 1)
+        E = offsets.numel() - 1
+    if Kcap is None:
+        Kcap = 128 * ((M + 127) // 128) if offsets is None else ragged_capacity(M, E)
+    q = _out(q, (M, 2 * I), torch.uint8, dev, "q")
+    s = _out(s, (2 * I // 128, M), torch.float32, dev, "s")
+    qt = _out(qt, (2 * I, Kcap), torch.uint8, dev, "qt")
+    st = _out(st, (Kcap // 128, 2 * I), torch.float32, dev, "st")
+    aqt = _out(aqt, (I, Kcap), torch.uint8, dev, "aqt")
+    ast = _out(ast, (Kcap // 128, I), torch.float32, dev, "ast")
+    _together(dev, (hq, "hq"), (hs, "hs"), (offsets, "offsets"), (q, "q"), (s, "s"), (qt, "qt"), (st, "st"),
+              (aqt, "aqt"), (ast, "ast"))
+    _launch("fp8q_swiglu_backward_quant", dev, _p(da), _p(hq), _p(hs), _p(offsets), E, M, I, _p(q), _p(s), _p(qt),
+            _p(st), _p(aqt), _p(ast), Kcap)
+    return q, s, qt, st, aqt, ast
 
 
 def device_status(device: torch.device | None = None) -> int:

@@ -72,8 +72,9 @@ enum {
     FP8Q_DEV_OK = 0,
     FP8Q_DEV_TIMEOUT = 1,      /* a bounded pipeline wait expired; the kernel exited early */
     FP8Q_DEV_BAD_OFFSETS = 2,  /* grouped GEMM: offsets not 0-based / nondecreasing / ending at Mtot */
-    FP8Q_DEV_BAD_SCALES = 3    /* fp8_gemm_blockscaled_ue8m0: a scale that is not a positive normal
+    FP8Q_DEV_BAD_SCALES = 3,   /* fp8_gemm_blockscaled_ue8m0: a scale that is not a positive normal
                                   power of two (its result is then unspecified) */
+    FP8Q_DEV_BAD_INDEX = 4     /* routed expert layer: an expert, slot or row index out of range */
 };
 
 /* Scale formats of the quantisers (the *_fmt entry points). */
@@ -326,6 +327,127 @@ FP8Q_API int fp8q_weight_128x128_fmt(const uint16_t* w, int64_t N, int64_t K, ui
 FP8Q_API int fp8_gemm_blockscaled_ue8m0(int mode, const uint8_t* A, const float* sA, const uint8_t* B,
                                         const float* sB, void* D, int64_t M, int64_t N, int64_t K,
                                         void* workspace, size_t ws_bytes, fp8q_stream_t stream);
+
+/*
+ * The operators of a routed expert layer (mixture of experts) around the grouped GEMMs.  The pages
+ * name the parts (sigmoid affinities, top-8 of 256 experts, a balance bias, SwiGLU inputs kept in
+ * low precision: [SUMMARY] Key ideas, Method; [REPOST] paragraph 1); the definitions are here.
+ *
+ *   fp8q_moe_route      logits -> each token's k experts and their weights
+ *   fp8q_moe_plan       experts of the T k slots -> the expert order of the rows
+ *   fp8q_moe_dispatch   tokens -> quantised rows in that order      -> grouped Fprop
+ *   fp8q_swiglu_quant   rows [gate | up] -> quantised rows of silu(gate) up, and the checkpoint
+ *                                                                   -> grouped Fprop
+ *   fp8q_moe_combine    rows -> tokens
+ * and backwards
+ *   fp8q_moe_dispatch (with the weights, of the output's gradient) -> grouped Dgrad, Wgrad
+ *   fp8q_moe_combine_dweight, fp8q_moe_route_backward                    the router's gradient
+ *   fp8q_swiglu_backward_quant (from the checkpoint)               -> grouped Dgrad, both Wgrads
+ *   fp8q_moe_combine (without weights)                                   the input's gradient
+ *
+ * Slot i = t k + j is choice j of token t.  Row r of the expert order holds slot slots[r], and slot
+ * i lies in row rows[i]; M = T k rows, expert e's are offsets[e] .. offsets[e+1]-1.  Index arrays,
+ * weights, logits and biases need the alignment of their element only; all else 16 bytes.
+ * Limits: E <= 1024, k <= 32, T k < 2^31 (FP8Q_ERR_UNSUPPORTED).  No output may overlap an input.
+ */
+enum { FP8Q_LOGITS_FP32 = 0, FP8Q_LOGITS_BF16 = 1 };
+enum { FP8Q_SCORE_SIGMOID = 0, FP8Q_SCORE_SOFTMAX = 1 };
+
+/*
+ * Routing.  logits [T, E] (fp32 or bf16), bias [E] fp32 or NULL -> idx [T, k], w [T, k] fp32.
+ *   score s = sigmoid(l), or softmax(l) over the token's experts;
+ *   key = s + bias, or without a bias the logit itself (the order of the scores);
+ *   the experts form n_group groups of E / n_group consecutive ones; a group's score is the sum of
+ *   its two largest keys (without a bias: its largest); the topk_group best groups are kept, and
+ *   the k best experts in them are chosen, in descending order.  Equal keys go to the lower index.
+ *   w_j = scale s_j / (sum of the chosen s) with renormalize, scale s_j without.  The bias never
+ *   enters w.
+ * The order is that of the keys in binary64, whatever the logits' type; w is rounded to fp32 once.
+ * A logit or bias of -inf masks its expert: it is chosen only where fewer than k unmasked experts are
+ * left in the kept groups, lowest index first, with weight 0.  A NaN or +inf masks the expert too,
+ * and makes all weights of the row NaN.  n_group <= 32, and E must be a multiple of it; scale is
+ * finite and not zero; k <= topk_group E / n_group (FP8Q_ERR_ARG).
+ */
+FP8Q_API int fp8q_moe_route(const void* logits, int logits_type, const float* bias_or_null, int64_t T, int32_t E,
+                            int32_t k, int32_t n_group, int32_t topk_group, int score, int renormalize, float scale,
+                            int32_t* idx, float* w, fp8q_stream_t stream);
+
+/*
+ * Gradient of the weights' loss with respect to the logits: dw [T, k], with w and idx as
+ * fp8q_moe_route returned them -> dlogits [T, E] in the logits' type, fully written.  The choice
+ * itself and the bias have no gradient.  A slot of weight 0 takes no part.  An expert outside [0, E)
+ * is left out and latches FP8Q_DEV_BAD_INDEX.
+ */
+FP8Q_API int fp8q_moe_route_backward(const float* dw, const float* w, const int32_t* idx, const void* logits,
+                                     int logits_type, int64_t T, int32_t E, int32_t k, int score, int renormalize,
+                                     float scale, void* dlogits, fp8q_stream_t stream);
+
+/*
+ * The expert order of the slots: idx [T, k] -> offsets [E + 1], slots [T k], rows [T, k].  Rows are
+ * ordered by expert, then by slot (a stable sort; the same expert twice in a token is two rows).  An
+ * expert outside [0, E) latches FP8Q_DEV_BAD_INDEX and gives the empty plan (offsets 0, slots and rows
+ * -1), which the readers refuse.  T == 0 writes offsets = 0.
+ */
+FP8Q_API int fp8q_moe_plan(const int32_t* idx, int64_t T, int32_t k, int32_t E, int32_t* offsets, int32_t* slots,
+                           int32_t* rows, fp8q_stream_t stream);
+
+/*
+ * Dispatch: row r of the expert order is v = weights[slots[r]] * x[slots[r] / k] (one fp32 product;
+ * x alone without weights), quantised from fp32.
+ *   x  : [T, C] bf16, weights : [T, k] fp32 or NULL
+ *   q  : [M, C] codes, s  : [C/128, M]       the 1x128 form, as fp8q_act_1x128 of the gathered rows
+ *   qt : [C, Kcap] codes, st : [Kcap/128, C] (both or neither NULL) the ragged 128x1 form, as
+ *        fp8q_act_128x1_transposed_ragged of the gathered rows; its tail is not written
+ * offsets, slots and rows come from one fp8q_moe_plan.  A slot or row index out of range latches
+ * FP8Q_DEV_BAD_INDEX: with qt its row is read as zeros, without it the row is not written.  With qt,
+ * malformed offsets, or Kcap too small, latch FP8Q_DEV_BAD_OFFSETS and nothing is written.
+ * C % 128 == 0, Kcap % 128 == 0.
+ */
+FP8Q_API int fp8q_moe_dispatch(const uint16_t* x, const int32_t* offsets, const int32_t* slots, const int32_t* rows,
+                               const float* weights_or_null, int32_t E, int64_t T, int32_t k, int64_t C, uint8_t* q,
+                               float* s, uint8_t* qt_or_null, float* st_or_null, int64_t Kcap, fp8q_stream_t stream);
+
+/*
+ * Combine: out[t] = add[t] + sum over j of weights[t, j] y[rows[t, j]], summed in fp32 in the order of
+ * j and rounded to bf16 once.  y : [M, C], add : [T, C] or NULL, out : [T, C], all bf16;
+ * weights : [T, k] fp32, or NULL for ones.  The row of a weight that is 0 is not read (an infinity
+ * there does no harm).  A row out of range is left out and latches FP8Q_DEV_BAD_INDEX.  C % 8 == 0.
+ */
+FP8Q_API int fp8q_moe_combine(const uint16_t* y, const int32_t* rows, const float* weights_or_null,
+                              const uint16_t* add_or_null, int64_t T, int32_t k, int64_t C, uint16_t* out,
+                              fp8q_stream_t stream);
+
+/* Gradient of fp8q_moe_combine's weights: dw[t, j] = <dout[t], y[rows[t, j]]>, fp32 sums.  A row out
+ * of range gives 0 and latches FP8Q_DEV_BAD_INDEX.  C % 8 == 0. */
+FP8Q_API int fp8q_moe_combine_dweight(const uint16_t* dout, const uint16_t* y, const int32_t* rows, int64_t T,
+                                      int32_t k, int64_t C, float* dw, fp8q_stream_t stream);
+
+/*
+ * SwiGLU between the two GEMMs of a feed-forward layer: a = silu(g) u with g = h[:, :I], u = h[:, I:].
+ *   h  : [M, 2 I] bf16
+ *   q  : [M, I] codes,   s  : [I/128, M]     a, quantised 1x128 from fp32
+ *   hq : [M, 2 I] codes, hs : [2 I/128, M]   (both or neither NULL) the checkpoint: h itself, as
+ *        fp8q_act_1x128(h), half the bytes of h
+ * I % 128 == 0; any M.  A NaN in h gives NaN codes; a group holding an infinity dequantises to NaN.
+ */
+FP8Q_API int fp8q_swiglu_quant(const uint16_t* h, int64_t M, int64_t I, uint8_t* q, float* s, uint8_t* hq_or_null,
+                               float* hs_or_null, fp8q_stream_t stream);
+
+/*
+ * SwiGLU backward from the checkpoint: with g, u = the dequantised halves of (hq, hs), r = sigmoid(g),
+ *   dh = [ da u r (1 + g (1 - r)),  da g r ],   a = g r u   (all fp32, quantised from there)
+ *   da : [M, I] bf16
+ *   q  : [M, 2 I], s  : [2 I/128, M]          dh, 1x128: the operand of Dgrad
+ *   qt : [2 I, Kcap], st : [Kcap/128, 2 I]    dh, ragged 128x1: the operand of the first GEMM's Wgrad
+ *   aqt: [I, Kcap], ast : [Kcap/128, I]       a, ragged 128x1: the operand of the second GEMM's Wgrad
+ * offsets : DEVICE int32 [E + 1], rows grouped by expert, as fp8q_act_128x1_transposed_ragged (the same
+ * tail and the same errors); or NULL with E = 1, one sequence of M rows (any M; Kcap >= M), whose
+ * last 128-row group is padded with zeros.  I % 128 == 0, Kcap % 128 == 0.
+ */
+FP8Q_API int fp8q_swiglu_backward_quant(const uint16_t* da, const uint8_t* hq, const float* hs,
+                                        const int32_t* offsets_or_null, int32_t E, int64_t M, int64_t I, uint8_t* q,
+                                        float* s, uint8_t* qt, float* st, uint8_t* aqt, float* ast, int64_t Kcap,
+                                        fp8q_stream_t stream);
 
 /*
  * Synchronise `stream`, then read and clear the device status word of the current device.
