@@ -148,12 +148,15 @@ int fp8q_moe_dispatch(const uint16_t* x, const int32_t* offsets, const int32_t* 
     if (!aligned4(offsets) || !aligned4(slots) || !aligned4(rows) || !aligned4(weights)) return FP8Q_ERR_ALIGN;
     const cudaStream_t cs = (cudaStream_t)stream;
     const int64_t M = T * k;
-    if (!qt)
-        return launch_kernel(moe_dispatch_rows_kernel, dim3(grid_for((M * (C / 128) + 31) / 32, 8)), dim3(256), 0, cs,
-                             false, x, rows, weights, T, (int)k, (int)C, q, s);
-    const int64_t tiles = ((M + 127) / 128 + E) * (C / 128);
-    return launch_kernel(moe_dispatch_both_kernel, dim3(grid_for(tiles, 2)), dim3(256), 0, cs, false, x, slots,
-                         weights, offsets, (int)E, M, (int)k, C, q, s, qt, st, Kcap);
+    const int64_t quads = T * ((C / 128 + 3) / 4), tiles = ((M + 127) / 128 + E) * (C / 128);
+    if (quads > kI32 || tiles > kI32) return FP8Q_ERR_UNSUPPORTED;
+    const auto by_row = weights ? moe_dispatch_rows_kernel<true> : moe_dispatch_rows_kernel<false>;
+    const int done = launch_kernel(by_row, dim3(grid_for((quads + 7) / 8, 8)), dim3(256), 0, cs, false, x, rows, weights,
+                                   (uint32_t)T, (uint32_t)k, (uint32_t)C, q, s, qt ? offsets : nullptr, (int)E, Kcap);
+    if (done != FP8Q_OK || !qt) return done;
+    const auto by_column = weights ? moe_dispatch_cols_kernel<true> : moe_dispatch_cols_kernel<false>;
+    return launch_kernel(by_column, dim3(grid_for((tiles + 7) / 8, weights ? 2 : 3)), dim3(256), 0, cs, false, x, slots, weights, offsets, (int)E,
+                         M, (int)k, (uint32_t)C, qt, st, Kcap);
 }
 
 int fp8q_moe_combine(const uint16_t* y, const int32_t* rows, const float* weights, const uint16_t* add, int64_t T,

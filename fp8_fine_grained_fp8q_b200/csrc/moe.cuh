@@ -380,9 +380,75 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const int32_t* _
     }
 }
 
+// The padded 128-row groups of expert-ordered rows (as act_128x1_t_ragged_kernel counts them).
+struct GroupTable {
+    int off[kMoeMaxExperts + 1];
+    int pre[kMoeMaxExperts + 1];
+    int bad;
+};
+
+// Fills the table (whole CTA; `offsets` null: one sequence of M rows).  False if the offsets are
+// malformed; FP8Q_DEV_BAD_OFFSETS is then latched.
+__device__ __forceinline__ bool group_table(GroupTable& t, const int32_t* __restrict__ offsets, int E, int64_t M,
+                                            int64_t Kcap)
+{
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (w == 0) {
+        if (offsets) {
+            for (int i = lane; i <= E; i += 32) t.off[i] = __ldg(offsets + i);
+        } else if (lane < 2) {
+            t.off[lane] = lane ? (int)M : 0;
+        }
+        __syncwarp();
+        const int per = (E + 31) >> 5;
+        const int lo = min(E, lane * per), hi = min(E, lo + per);
+        int local = 0;
+        bool bad = false;
+        for (int e = lo; e < hi; ++e) {
+            const int64_t cnt = (int64_t)t.off[e + 1] - t.off[e];
+            bad |= cnt < 0 || cnt > M;
+            local += cnt > 0 && cnt <= M ? (int)((cnt + 127) >> 7) : 0;
+        }
+        int incl = local;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
+        }
+        int run = incl - local;
+        for (int e = lo; e < hi; ++e) {
+            t.pre[e] = run;
+            const int64_t cnt = (int64_t)t.off[e + 1] - t.off[e];
+            run += cnt > 0 && cnt <= M ? (int)((cnt + 127) >> 7) : 0;
+        }
+        if (lane == 31) {
+            t.pre[E] = incl;
+            bad |= t.off[0] != 0 || (int64_t)t.off[E] != M || (int64_t)incl * 128 > Kcap;
+        }
+        bad = __any_sync(kFull, bad);
+        if (lane == 0) t.bad = bad ? 1 : 0;
+    }
+    __syncthreads();
+    if (t.bad && threadIdx.x == 0) latch_status(kDevBadOffsets);
+    return !t.bad;
+}
+
+// First row and number of rows of padded group g < pre[E].
+__device__ __forceinline__ void group_rows(const GroupTable& t, int E, int g, int64_t& r0, int& nvalid)
+{
+    int lo = 0, hi = E;   // pre[lo] <= g < pre[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.pre[mid] <= g) lo = mid; else hi = mid;
+    }
+    r0 = (int64_t)t.off[lo] + 128ll * (g - t.pre[lo]);
+    nvalid = (int)min((int64_t)128, (int64_t)t.off[lo + 1] - r0);
+}
+
 // ------------------------------------------------------------------------------------------
-// Dispatch, 1x128 codes only: v[r] = (weight of slot) * x[slot / k], quantised where it lands.
-// Eight lanes own one 128-element tile of one slot.
+// Dispatch, 1x128 codes: row rows[t,j] holds (weight of the slot) * x[t].  A warp takes four 128-element
+// tiles of one token (eight lanes each), reads them once and writes them to the token's k rows: bound
+// by the writes.  Without weights the k rows hold the same codes, which are formed once.
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&f)[16])
 {
@@ -417,43 +483,99 @@ __device__ __forceinline__ float max8(float v)
     return v;
 }
 
+// Two FP32 products at once (mul.rn.f32x2: each rounded to nearest, as __fmul_rn).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 c, a, b;\n\t"
+        "mov.b64 {%0, %1}, c;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 widen(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ uint32_t abs2(uint32_t w) { return w & 0x7FFF7FFFu; }
+// Larger of each of two bf16 pairs; a NaN loses, as in fmaxf.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+template <bool WEIGHTED>
 __global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* __restrict__ x,
                                                                 const int32_t* __restrict__ rows,
-                                                                const float* __restrict__ weights, int64_t T, int k,
-                                                                int C, uint8_t* __restrict__ q,
-                                                                float* __restrict__ s)
+                                                                const float* __restrict__ weights, uint32_t T,
+                                                                uint32_t k, uint32_t C, uint8_t* __restrict__ q,
+                                                                float* __restrict__ s,
+                                                                const int32_t* __restrict__ offsets, int E,
+                                                                int64_t Kcap)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t M = T * k;
-    const int CB = C >> 7;
-    const int64_t tiles = M * CB;
-    const int sub = threadIdx.x & 7;
-    const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 3;
-    const int64_t first = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
-    for (int64_t b = first - (first & 3); b < tiles; b += step) {   // warp-uniform: 4 tiles a warp
-        const int64_t i = b + (first & 3);
-        const bool live = i < tiles;
-        const int64_t slot = live ? i / CB : 0;
-        const int kb = live ? (int)(i - slot * CB) : 0;
-        float f[16];
-        const uint4* p = reinterpret_cast<const uint4*>(x + (slot / k) * C + kb * 128) + 2 * sub;
-        unpack16(__ldg(p), __ldg(p + 1), f);
-        if (weights) {
-            const float wt = weights[slot];
+    if (offsets) {   // the 128x1 form follows: write neither if it will refuse the offsets
+        __shared__ GroupTable table;
+        if (!group_table(table, offsets, E, (int64_t)T * k, Kcap)) return;
+    }
+    const uint32_t M = T * k, CB = C >> 7, quads = (CB + 3) >> 2, items = T * quads;
+    const int lane = threadIdx.x & 31, sub = lane & 7;
+    const uint32_t warps = (gridDim.x * blockDim.x) >> 5;
+    for (uint32_t it = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items; it += warps) {
+        const uint32_t t = it / quads, kb = (it - t * quads) * 4 + (lane >> 3);
+        const bool live = kb < CB;
+        int32_t row = -1;
+        float wt = 1.0f;
+        if (lane < k) {
+            row = __ldg(rows + t * k + lane);
+            if (WEIGHTED) wt = __ldg(weights + t * k + lane);
+            if (row < 0 || row >= (int32_t)M) {
+                latch_status(kDevBadIndex);
+                row = -1;
+            }
+        }
+        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+        if (live) {
+            const uint4* p = reinterpret_cast<const uint4*>(x + (size_t)t * C + kb * 128) + 2 * sub;
+            a = __ldg(p);
+            b = __ldg(p + 1);
+        }
+        const float amax = max8(amax16(a, b));
+        uint8_t* qb = q + kb * 128 + 16 * sub;
+        float* sb = s + (size_t)kb * M;
+        if (!WEIGHTED) {
+            float sc, inv;
+            group_scale<false>(amax, sc, inv);
+            const uint2 lo = quant8(a, inv), hi = quant8(b, inv);
+            for (uint32_t j = 0; j < k; ++j) {
+                const int32_t r = __shfl_sync(kFull, row, j);
+                if (r < 0 || !live) continue;
+                *reinterpret_cast<uint4*>(qb + (size_t)r * C) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                if (sub == 0) sb[r] = sc;
+            }
+        } else {
+            const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            for (uint32_t j = 0; j < k; ++j) {
+                const int32_t r = __shfl_sync(kFull, row, j);
+                const float wj = __shfl_sync(kFull, wt, j);
+                // |w| max|x| is the largest |w x|: rounding keeps the order.
+                float sc, inv;
+                group_scale<false>(__fmul_rn(fabsf(wj), amax), sc, inv);
+                if (r < 0 || !live) continue;
+                uint32_t c[4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = __fmul_rn(wt, f[j]);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 w2 = make_float2(wj, wj), i2 = make_float2(inv, inv);
+                    const float2 lo = mul2(mul2(widen(u[2 * i]), w2), i2), hi = mul2(mul2(widen(u[2 * i + 1]), w2), i2);
+                    c[i] = e4m3x2(lo.x, lo.y) | (e4m3x2(hi.x, hi.y) << 16);
+                }
+                *reinterpret_cast<uint4*>(qb + (size_t)r * C) = make_uint4(c[0], c[1], c[2], c[3]);
+                if (sub == 0) sb[r] = sc;
+            }
         }
-        float sc, inv;
-        group_scale<false>(max8(amax16f(f)), sc, inv);
-        if (!live) continue;
-        const int32_t r = rows[slot];
-        if (r < 0 || r >= M) {
-            latch_status(kDevBadIndex);
-            continue;
-        }
-        reinterpret_cast<uint4*>(q + (int64_t)r * C + kb * 128)[sub] = quant16f(f, inv);
-        if (sub == 0) s[(int64_t)kb * M + r] = sc;
     }
 }
 
@@ -538,114 +660,150 @@ __device__ __forceinline__ void tile_cols(const float (&v)[16][4], int64_t g, in
     __syncthreads();
 }
 
-// The padded 128-row groups of expert-ordered rows (as act_128x1_t_ragged_kernel counts them).
-struct GroupTable {
-    int off[kMoeMaxExperts + 1];
-    int pre[kMoeMaxExperts + 1];
-    int bad;
+// ------------------------------------------------------------------------------------------
+// Dispatch, ragged 128x1 codes.  A warp takes one padded group (128 rows) x 16 channels at a time: lane
+// (r, h) = (lane >> 1, lane & 1) holds rows 8r .. 8r+7 of channels 8h .. 8h+7, gathered from x as bf16.
+// The column maxima need shuffles only, and a channel's 128 codes leave as one line, 8 bytes from
+// each r: no shared memory and no barrier.  The warp keeps its tokens over kColSlices slices.
+// Bound by the writes, with the arithmetic close behind.  Tiles are ordered by channel block first: at
+// any time the whole grid gathers from a few channel blocks of x (2 MB per 128 channels of 8192 tokens),
+// so a token's k reads find it in L2 although x as a whole need not fit.
+// ------------------------------------------------------------------------------------------
+constexpr int kColSlices = 8;   // 16-channel slices of a tile
+
+// Larger magnitude of each of two bf16 pairs, its sign unspecified; a NaN loses.
+__device__ __forceinline__ uint32_t maxabs2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Quantises one 16-channel slice: m[j] = max|.| of the lane's rows in channels 8h + j, f(j, i) = row i's
+// value there; codes to `out` (this lane's 8 bytes of channel 8h), scales to `st`.
+struct ColScale {
+    float inv[8];
 };
-
-// Fills the table (whole CTA; `offsets` null: one sequence of M rows).  False if the offsets are
-// malformed; FP8Q_DEV_BAD_OFFSETS is then latched.
-__device__ __forceinline__ bool group_table(GroupTable& t, const int32_t* __restrict__ offsets, int E, int64_t M,
-                                            int64_t Kcap)
+__device__ __forceinline__ ColScale column_scales(float (&m)[8], int lane, float* __restrict__ st)
 {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (w == 0) {
-        if (offsets) {
-            for (int i = lane; i <= E; i += 32) t.off[i] = __ldg(offsets + i);
-        } else if (lane < 2) {
-            t.off[lane] = lane ? (int)M : 0;
-        }
-        __syncwarp();
-        const int per = (E + 31) >> 5;
-        const int lo = min(E, lane * per), hi = min(E, lo + per);
-        int local = 0;
-        bool bad = false;
-        for (int e = lo; e < hi; ++e) {
-            const int64_t cnt = (int64_t)t.off[e + 1] - t.off[e];
-            bad |= cnt < 0 || cnt > M;
-            local += cnt > 0 && cnt <= M ? (int)((cnt + 127) >> 7) : 0;
-        }
-        int incl = local;
+    // Reduce over r (lane bits 1..4).  Bits 1..3 scatter: afterwards r holds channel 8h + (r & 7).
+    const bool b0 = lane & 2, b1 = lane & 4, b2 = lane & 8;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, incl, o);
-            if (lane >= o) incl += y;
-        }
-        int run = incl - local;
-        for (int e = lo; e < hi; ++e) {
-            t.pre[e] = run;
-            const int64_t cnt = (int64_t)t.off[e + 1] - t.off[e];
-            run += cnt > 0 && cnt <= M ? (int)((cnt + 127) >> 7) : 0;
-        }
-        if (lane == 31) {
-            t.pre[E] = incl;
-            bad |= t.off[0] != 0 || (int64_t)t.off[E] != M || (int64_t)incl * 128 > Kcap;
-        }
-        bad = __any_sync(kFull, bad);
-        if (lane == 0) t.bad = bad ? 1 : 0;
+    for (int j = 0; j < 4; ++j) {
+        const float send = b2 ? m[j] : m[j + 4], keep = b2 ? m[j + 4] : m[j];
+        m[j] = fmaxf(keep, __shfl_xor_sync(kFull, send, 8));
     }
-    __syncthreads();
-    if (t.bad && threadIdx.x == 0) latch_status(kDevBadOffsets);
-    return !t.bad;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float send = b1 ? m[j] : m[j + 2], keep = b1 ? m[j + 2] : m[j];
+        m[j] = fmaxf(keep, __shfl_xor_sync(kFull, send, 4));
+    }
+    {
+        const float send = b0 ? m[0] : m[1], keep = b0 ? m[1] : m[0];
+        m[0] = fmaxf(keep, __shfl_xor_sync(kFull, send, 2));
+    }
+    m[0] = fmaxf(m[0], __shfl_xor_sync(kFull, m[0], 16));
+    float sc, inv;
+    group_scale<false>(m[0], sc, inv);
+    if (lane < 16) st[8 * (lane & 1) + (lane >> 1)] = sc;
+    ColScale r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.inv[j] = __shfl_sync(kFull, inv, 2 * j + (lane & 1));
+    return r;
 }
 
-// First row and number of rows of padded group g < pre[E].
-__device__ __forceinline__ void group_rows(const GroupTable& t, int E, int g, int64_t& r0, int& nvalid)
-{
-    int lo = 0, hi = E;   // pre[lo] <= g < pre[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (t.pre[mid] <= g) lo = mid; else hi = mid;
-    }
-    r0 = (int64_t)t.off[lo] + 128ll * (g - t.pre[lo]);
-    nvalid = (int)min((int64_t)128, (int64_t)t.off[lo + 1] - r0);
-}
-
-// Dispatch, both forms: tiles of one padded group x 128 channels, the channel block in the outer
-// loop: at any time the whole grid gathers from a few channel blocks of x, so a token's k reads find
-// it in L2 although x as a whole need not fit.
-__global__ void __launch_bounds__(256, 2) moe_dispatch_both_kernel(
+template <bool WEIGHTED>
+__global__ void __launch_bounds__(256, WEIGHTED ? 2 : 3) moe_dispatch_cols_kernel(
     const uint16_t* __restrict__ x, const int32_t* __restrict__ slots, const float* __restrict__ weights,
-    const int32_t* __restrict__ offsets, int E, int64_t M, int k, int64_t C, uint8_t* __restrict__ q,
-    float* __restrict__ s, uint8_t* __restrict__ qt, float* __restrict__ st, int64_t Kcap)
+    const int32_t* __restrict__ offsets, int E, int64_t M, int k, uint32_t C, uint8_t* __restrict__ qt,
+    float* __restrict__ st, int64_t Kcap)
 {
     griddep_launch_dependents();
     griddep_wait();
     __shared__ GroupTable table;
-    __shared__ __align__(16) TileScratch sm;
     if (!group_table(table, offsets, E, M, Kcap)) return;
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t groups = table.pre[E], tiles = groups * (C >> 7);
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t cb = tile / groups;
-        const int g = (int)(tile - cb * groups);
+    const int lane = threadIdx.x & 31, r = lane >> 1, h = lane & 1;
+    const uint32_t groups = table.pre[E], tiles = groups * (C >> 7);
+    const uint32_t warps = (gridDim.x * blockDim.x) >> 5;
+    for (uint32_t tile = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; tile < tiles; tile += warps) {
+        const uint32_t cb = tile / groups, g = tile - cb * groups;
         int64_t r0;
         int nvalid;
-        group_rows(table, E, g, r0, nvalid);
-        float v[16][4];
+        group_rows(table, E, (int)g, r0, nvalid);
+        int token[8];
+        float wt[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int n = 16 * w + i;
-            uint2 u = make_uint2(0u, 0u);
-            float wt = 1.0f;
-            if (n < nvalid) {
-                const int32_t slot = __ldg(slots + r0 + n);
+        for (int i = 0; i < 8; ++i) {
+            token[i] = -1;
+            wt[i] = 0.0f;
+            if (8 * r + i < nvalid) {
+                const int32_t slot = __ldg(slots + r0 + 8 * r + i);
                 if (slot >= 0 && slot < M) {
-                    u = __ldg(reinterpret_cast<const uint2*>(x + (int64_t)(slot / k) * C + cb * 128) + lane);
-                    if (weights) wt = __ldg(weights + slot);
-                } else if (lane == 0) {
+                    token[i] = slot / k;
+                    if (WEIGHTED) wt[i] = __ldg(weights + slot);
+                } else {
                     latch_status(kDevBadIndex);
                 }
             }
-            v[i][0] = __fmul_rn(wt, bf16_lo(u.x));
-            v[i][1] = __fmul_rn(wt, bf16_hi(u.x));
-            v[i][2] = __fmul_rn(wt, bf16_lo(u.y));
-            v[i][3] = __fmul_rn(wt, bf16_hi(u.y));
         }
-        tile_rows(v, nvalid, r0, cb * 128, M, C, q, s);
-        tile_cols(v, g, cb * 128, C, Kcap, qt, st, sm);
+        uint8_t* out = qt + (int64_t)(cb * 128 + 8 * h) * Kcap + (int64_t)g * 128 + 8 * r;
+        float* sc = st + (uint64_t)g * C + cb * 128;
+        const uint16_t* src = x + cb * 128 + 8 * h;
+#pragma unroll 1
+        for (int sl = 0; sl < kColSlices; ++sl, src += 16, out += 16 * Kcap, sc += 16) {
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (token[i] >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(src + (uint64_t)(uint32_t)token[i] * C));
+            }
+            float m[8];
+            float2 f[4][8];   // weighted: the products, formed once
+            if (WEIGHTED) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    m[2 * j] = m[2 * j + 1] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t u = j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w;
+                        f[j][i] = mul2(widen(u), make_float2(wt[i], wt[i]));
+                        m[2 * j] = fmaxf(m[2 * j], fabsf(f[j][i].x));
+                        m[2 * j + 1] = fmaxf(m[2 * j + 1], fabsf(f[j][i].y));
+                    }
+                }
+            } else {
+                uint32_t p[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[0] = maxabs2(p[0], v[i].x);
+                    p[1] = maxabs2(p[1], v[i].y);
+                    p[2] = maxabs2(p[2], v[i].z);
+                    p[3] = maxabs2(p[3], v[i].w);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    m[2 * j] = fabsf(bf16_lo(p[j]));
+                    m[2 * j + 1] = fabsf(bf16_hi(p[j]));
+                }
+            }
+            const ColScale cs = column_scales(m, lane, sc);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {   // channels 8h + 2j, + 1
+                const float2 inv = make_float2(cs.inv[2 * j], cs.inv[2 * j + 1]);
+                float2 y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t u = j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w;
+                    y[i] = mul2(WEIGHTED ? f[j][i] : widen(u), inv);
+                }
+                *reinterpret_cast<uint2*>(out + (2 * j) * Kcap) =
+                    make_uint2(e4m3x2(y[0].x, y[1].x) | (e4m3x2(y[2].x, y[3].x) << 16),
+                               e4m3x2(y[4].x, y[5].x) | (e4m3x2(y[6].x, y[7].x) << 16));
+                *reinterpret_cast<uint2*>(out + (2 * j + 1) * Kcap) =
+                    make_uint2(e4m3x2(y[0].y, y[1].y) | (e4m3x2(y[2].y, y[3].y) << 16),
+                               e4m3x2(y[4].y, y[5].y) | (e4m3x2(y[6].y, y[7].y) << 16));
+            }
+        }
     }
 }
 

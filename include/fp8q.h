@@ -398,9 +398,10 @@ FP8Q_API int fp8q_moe_plan(const int32_t* idx, int64_t T, int32_t k, int32_t E, 
  *   q  : [M, C] codes, s  : [C/128, M]       the 1x128 form, as fp8q_act_1x128 of the gathered rows
  *   qt : [C, Kcap] codes, st : [Kcap/128, C] (both or neither NULL) the ragged 128x1 form, as
  *        fp8q_act_128x1_transposed_ragged of the gathered rows; its tail is not written
- * offsets, slots and rows come from one fp8q_moe_plan.  A slot or row index out of range latches
- * FP8Q_DEV_BAD_INDEX: with qt its row is read as zeros, without it the row is not written.  With qt,
- * malformed offsets, or Kcap too small, latch FP8Q_DEV_BAD_OFFSETS and nothing is written.
+ * offsets, slots and rows come from one fp8q_moe_plan.  An index out of range latches
+ * FP8Q_DEV_BAD_INDEX: a bad entry of rows leaves a row of the 1x128 form unwritten, a bad entry of
+ * slots is a row of zeros in the 128x1 form.  With qt, malformed offsets, or Kcap too small, latch
+ * FP8Q_DEV_BAD_OFFSETS and nothing is written.
  * C % 128 == 0, Kcap % 128 == 0.
  */
 FP8Q_API int fp8q_moe_dispatch(const uint16_t* x, const int32_t* offsets, const int32_t* slots, const int32_t* rows,

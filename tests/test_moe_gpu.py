@@ -268,17 +268,33 @@ def test_dispatch_is_the_quantisers_of_the_gathered_rows(T, k, E, C, weighted):
     assert bool((qt[:, K:] == 0xA5).all()) and bool(torch.isnan(st[K // 128:]).all()), "the tail was written"
 
 
-def test_dispatch_nan_and_infinity_show():
-    x = np.zeros((2, 128), np.float32)
-    x[0, 3], x[0, 4] = NAN, 2.0
-    x[1, 7] = INF
+@pytest.mark.parametrize("weighted", [False, True])
+def test_dispatch_nan_and_infinity_show(weighted):
+    x = np.zeros((3, 128), np.float32)
+    x[0, 3], x[0, 4], x[0, 100] = NAN, 2.0, -NAN
+    x[1, 7], x[1, 8] = INF, -3.0
+    x[2, 3], x[2, 4] = 5.0, NAN
     t, _ = bf16(x)
-    plan = make_plan(np.zeros((2, 1), np.int32), 1)
-    q, s, _, _ = ops.moe_dispatch(t, plan)
-    ok()
-    d = host(q).astype(np.uint8)
-    got = oracle.e4m3_decode(d.reshape(-1)).reshape(d.shape) * host(s).T
-    assert np.isnan(got[0, 3]) and abs(got[0, 4] - 2.0) < 0.01 and np.isnan(got[1, 7])
+    idx = np.zeros((3, 1), np.int32)
+    w = f32_dev(np.ones((3, 1), np.float32)) if weighted else None
+    for both in (False, True):
+        q, s, qt, st = ops.moe_dispatch(t, make_plan(idx, 1), weights=w, transposed=both)
+        ok()
+        v = t.float().cpu().numpy()
+        wq, ws = _moe.quant_rows(v)
+        same_bits(s, ws, "scales")
+        # A NaN stays one and does not touch its neighbours; an infinity makes its group's scale infinite, and
+        # with it the whole group NaN.
+        with np.errstate(invalid="ignore"):
+            got, want = _moe.decode_rows(host(q), host(s)), _moe.decode_rows(wq, ws)
+            assert np.array_equal(got, want, equal_nan=True)
+            assert np.isnan(got[[0, 0, 1, 2], [3, 100, 7, 4]]).all() and np.isnan(got).sum() == 3 + 128
+            if both:
+                wq, ws = _moe.quant_cols(v, np.array([0, 3]))
+                same_bits(st[:1], ws, "column scales")
+                got, want = _moe.decode_cols(host(qt)[:, :128], host(st)[:1]), _moe.decode_cols(wq, ws)
+                assert np.array_equal(got, want, equal_nan=True)
+                assert abs(got[3, 2] - 5.0) < 1e-6 and np.isnan(got[3, 0]) and np.isnan(got[7, 1])
 
 
 def test_dispatch_bad_plans():
@@ -293,8 +309,9 @@ def test_dispatch_bad_plans():
     assert (host(q)[rows[3, 1]] == 0xA5).all() and np.isnan(host(s)[:, rows[3, 1]]).all()
     bad = slots.copy()
     bad[5] = -7
-    q, _, _, _ = dispatch(bits, ops.MoePlan(i32(off), i32(bad), i32(rows)))
-    assert ops.device_status() == ops.DEV_BAD_INDEX and not host(q)[5].any()
+    _, _, qt, _ = dispatch(bits, ops.MoePlan(i32(off), i32(bad), i32(rows)))
+    at = [128 * g + r for g, n in enumerate(np.diff(off)) for r in range(n)]       # padded columns of the rows
+    assert ops.device_status() == ops.DEV_BAD_INDEX and not host(qt)[:, at[5]].any() and host(qt)[:, at[4]].any()
     for o in ([0, 5, 3, 30, 40], [1, 5, 9, 30, 40], [0, 5, 9, 30, 41], [0, -2000000000, 2000000000, 30, 40]):
         q, s, qt, st = dispatch(bits, ops.MoePlan(i32(o), i32(slots), i32(rows)))
         assert ops.device_status() == ops.DEV_BAD_OFFSETS
