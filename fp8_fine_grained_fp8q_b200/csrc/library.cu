@@ -13,6 +13,16 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 constexpr int64_t kI32 = 0x7FFFFFFF;
 
+// Division of n < 2^31 by d as (umulhi(n, mul) + n) >> shift: with 2^shift the smallest power of two not
+// below d, mul = floor(2^32 (2^shift - d) / d) + 1 (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994).
+FastDiv fast_div(uint32_t d)
+{
+    uint32_t shift = 0;
+    while ((1ull << shift) < d) ++shift;
+    return FastDiv{(uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1), shift};
+}
+
 // A persistent grid: `per_sm` CTAs on each SM, no more than there are work items.
 unsigned grid_for(int64_t items, int per_sm)
 {
@@ -151,12 +161,17 @@ int fp8q_moe_dispatch(const uint16_t* x, const int32_t* offsets, const int32_t* 
     const int64_t quads = T * ((C / 128 + 3) / 4), tiles = ((M + 127) / 128 + E) * (C / 128);
     if (quads > kI32 || tiles > kI32) return FP8Q_ERR_UNSUPPORTED;
     const auto by_row = weights ? moe_dispatch_rows_kernel<true> : moe_dispatch_rows_kernel<false>;
-    const int done = launch_kernel(by_row, dim3(grid_for((quads + 7) / 8, 8)), dim3(256), 0, cs, false, x, rows, weights,
-                                   (uint32_t)T, (uint32_t)k, (uint32_t)C, q, s, qt ? offsets : nullptr, (int)E, Kcap);
+    const int done = launch_kernel(by_row, dim3(grid_for((quads + 7) / 8, 8)), dim3(256), qt ? group_table_bytes(E) : 0, cs,
+                                   false, x, rows, weights, (uint32_t)T, (uint32_t)k, (uint32_t)C, q, s,
+                                   qt ? offsets : nullptr, (int)E, Kcap);
     if (done != FP8Q_OK || !qt) return done;
+    const int64_t items = ((M + 127) / 128 + E) * ((C / 128 + kColBlocks - 1) / kColBlocks);
     const auto by_column = weights ? moe_dispatch_cols_kernel<true> : moe_dispatch_cols_kernel<false>;
-    return launch_kernel(by_column, dim3(grid_for((tiles + 7) / 8, weights ? 2 : 3)), dim3(256), 0, cs, false, x, slots, weights, offsets, (int)E,
-                         M, (int)k, (uint32_t)C, qt, st, Kcap);
+    if (cudaFuncSetAttribute(by_column, cudaFuncAttributeMaxDynamicSharedMemorySize, gather_smem(kMoeMaxExperts)) !=
+        cudaSuccess)
+        return FP8Q_ERR_CUDA;
+    return launch_kernel(by_column, dim3(grid_for(items, 3)), dim3(256), gather_smem(E), cs, false, x, slots, weights,
+                         offsets, (int)E, M, fast_div((uint32_t)k), (uint32_t)C, qt, st, Kcap);
 }
 
 int fp8q_moe_combine(const uint16_t* y, const int32_t* rows, const float* weights, const uint16_t* add, int64_t T,
@@ -213,7 +228,7 @@ int fp8q_swiglu_backward_quant(const uint16_t* da, const uint8_t* hq, const floa
         !aligned16(st) || !aligned16(aqt) || !aligned16(ast) || !aligned4(offsets))
         return FP8Q_ERR_ALIGN;
     const int64_t tiles = ((M + 127) / 128 + E) * (I / 128);
-    return launch_kernel(swiglu_backward_kernel, dim3(grid_for(tiles, 2)), dim3(256), 0, (cudaStream_t)stream, false,
+    return launch_kernel(swiglu_backward_kernel, dim3(grid_for(tiles, 2)), dim3(256), group_table_bytes(E), (cudaStream_t)stream, false,
                          da, hq, hs, offsets, (int)E, M, I, q, s, qt, st, aqt, ast, Kcap);
 }
 

@@ -380,16 +380,21 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const int32_t* _
     }
 }
 
-// The padded 128-row groups of expert-ordered rows (as act_128x1_t_ragged_kernel counts them).
+// The padded 128-row groups of expert-ordered rows (as act_128x1_t_ragged_kernel counts them), in
+// shared memory of group_table_bytes(E): E + 1 offsets, E + 1 counts of the groups before an expert,
+// one flag.
+constexpr int group_table_bytes(int E) { return ((2 * (E + 1) + 1) * 4 + 15) & ~15; }
 struct GroupTable {
-    int off[kMoeMaxExperts + 1];
-    int pre[kMoeMaxExperts + 1];
-    int bad;
+    int* off;
+    int* pre;
+    int* bad;
+    __device__ GroupTable(void* smem, int E)
+        : off(static_cast<int*>(smem)), pre(off + E + 1), bad(pre + E + 1) {}
 };
 
 // Fills the table (whole CTA; `offsets` null: one sequence of M rows).  False if the offsets are
 // malformed; FP8Q_DEV_BAD_OFFSETS is then latched.
-__device__ __forceinline__ bool group_table(GroupTable& t, const int32_t* __restrict__ offsets, int E, int64_t M,
+__device__ __forceinline__ bool group_table(const GroupTable& t, const int32_t* __restrict__ offsets, int E, int64_t M,
                                             int64_t Kcap)
 {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -426,11 +431,11 @@ __device__ __forceinline__ bool group_table(GroupTable& t, const int32_t* __rest
             bad |= t.off[0] != 0 || (int64_t)t.off[E] != M || (int64_t)incl * 128 > Kcap;
         }
         bad = __any_sync(kFull, bad);
-        if (lane == 0) t.bad = bad ? 1 : 0;
+        if (lane == 0) *t.bad = bad ? 1 : 0;
     }
     __syncthreads();
-    if (t.bad && threadIdx.x == 0) latch_status(kDevBadOffsets);
-    return !t.bad;
+    if (*t.bad && threadIdx.x == 0) latch_status(kDevBadOffsets);
+    return !*t.bad;
 }
 
 // First row and number of rows of padded group g < pre[E].
@@ -466,9 +471,21 @@ __device__ __forceinline__ float amax16f(const float (&f)[16])
     for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
     return m;
 }
+// Four codes of four values, the first in the low byte.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d)
+{
+    uint32_t r;
+    asm("{.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float inv)
 {
-    return e4m3x2(__fmul_rn(a, inv), __fmul_rn(b, inv)) | (e4m3x2(__fmul_rn(c, inv), __fmul_rn(d, inv)) << 16);
+    return codes4(__fmul_rn(a, inv), __fmul_rn(b, inv), __fmul_rn(c, inv), __fmul_rn(d, inv));
 }
 __device__ __forceinline__ uint4 quant16f(const float (&f)[16], float inv)
 {
@@ -518,8 +535,8 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* 
     griddep_launch_dependents();
     griddep_wait();
     if (offsets) {   // the 128x1 form follows: write neither if it will refuse the offsets
-        __shared__ GroupTable table;
-        if (!group_table(table, offsets, E, (int64_t)T * k, Kcap)) return;
+        extern __shared__ __align__(16) uint8_t smem[];
+        if (!group_table(GroupTable(smem, E), offsets, E, (int64_t)T * k, Kcap)) return;
     }
     const uint32_t M = T * k, CB = C >> 7, quads = (CB + 3) >> 2, items = T * quads;
     const int lane = threadIdx.x & 31, sub = lane & 7;
@@ -570,7 +587,7 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* 
                 for (int i = 0; i < 4; ++i) {
                     const float2 w2 = make_float2(wj, wj), i2 = make_float2(inv, inv);
                     const float2 lo = mul2(mul2(widen(u[2 * i]), w2), i2), hi = mul2(mul2(widen(u[2 * i + 1]), w2), i2);
-                    c[i] = e4m3x2(lo.x, lo.y) | (e4m3x2(hi.x, hi.y) << 16);
+                    c[i] = codes4(lo.x, lo.y, hi.x, hi.y);
                 }
                 *reinterpret_cast<uint4*>(qb + (size_t)r * C) = make_uint4(c[0], c[1], c[2], c[3]);
                 if (sub == 0) sb[r] = sc;
@@ -661,15 +678,26 @@ __device__ __forceinline__ void tile_cols(const float (&v)[16][4], int64_t g, in
 }
 
 // ------------------------------------------------------------------------------------------
-// Dispatch, ragged 128x1 codes.  A warp takes one padded group (128 rows) x 16 channels at a time: lane
-// (r, h) = (lane >> 1, lane & 1) holds rows 8r .. 8r+7 of channels 8h .. 8h+7, gathered from x as bf16.
-// The column maxima need shuffles only, and a channel's 128 codes leave as one line, 8 bytes from
-// each r: no shared memory and no barrier.  The warp keeps its tokens over kColSlices slices.
+// Dispatch, ragged 128x1 codes.  A CTA takes tiles of one padded group (128 rows) x 128 channels; the
+// gathered rows come into shared memory by asynchronous copies, 256 bytes of a row at a time, while the
+// previous tile is quantised.  Warp w quantises channels 16w .. 16w+15: lane (r, h) = (lane >> 1,
+// lane & 1) holds rows 8r .. 8r+7 of channels 8h .. 8h+7, so the column maxima need shuffles only, and a
+// channel's 128 codes leave as one line, 8 bytes from each r.  One barrier a tile.
 // Bound by the writes, with the arithmetic close behind.  Tiles are ordered by channel block first: at
 // any time the whole grid gathers from a few channel blocks of x (2 MB per 128 channels of 8192 tokens),
 // so a token's k reads find it in L2 although x as a whole need not fit.
 // ------------------------------------------------------------------------------------------
-constexpr int kColSlices = 8;   // 16-channel slices of a tile
+// 16-byte piece c of row r of a staged tile (256 bytes a row) lies at piece c ^ 2 ((r >> 3) & 3) of the
+// row: the four r of a quarter-warp then read different banks.
+__device__ __forceinline__ uint32_t stage_at(int r, int c) { return r * 256 + ((c ^ (((r >> 3) & 3) << 1)) << 4); }
+
+constexpr int kStageBytes = 128 * 256;
+constexpr int gather_smem(int E) { return 2 * kStageBytes + 3 * 1024 + group_table_bytes(E); }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live)   // zeros unless live
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
 
 // Larger magnitude of each of two bf16 pairs, its sign unspecified; a NaN loses.
 __device__ __forceinline__ uint32_t maxabs2(uint32_t a, uint32_t b)
@@ -678,15 +706,12 @@ __device__ __forceinline__ uint32_t maxabs2(uint32_t a, uint32_t b)
     asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 
-// Quantises one 16-channel slice: m[j] = max|.| of the lane's rows in channels 8h + j, f(j, i) = row i's
-// value there; codes to `out` (this lane's 8 bytes of channel 8h), scales to `st`.
-struct ColScale {
-    float inv[8];
-};
-__device__ __forceinline__ ColScale column_scales(float (&m)[8], int lane, float* __restrict__ st)
+// Scales of a warp's 16 columns from m[j], the largest magnitude in this lane's rows of column 8h + j:
+// stores them (lanes r < 8: column 8h + r) and returns in m the factors 1 / scale of columns 8h + j.
+__device__ __forceinline__ void column_scales(float (&m)[8], int lane, float* __restrict__ st)
 {
-    // Reduce over r (lane bits 1..4).  Bits 1..3 scatter: afterwards r holds channel 8h + (r & 7).
     const bool b0 = lane & 2, b1 = lane & 4, b2 = lane & 8;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -698,111 +723,187 @@ __device__ __forceinline__ ColScale column_scales(float (&m)[8], int lane, float
         const float send = b1 ? m[j] : m[j + 2], keep = b1 ? m[j + 2] : m[j];
         m[j] = fmaxf(keep, __shfl_xor_sync(kFull, send, 4));
     }
-    {
-        const float send = b0 ? m[0] : m[1], keep = b0 ? m[1] : m[0];
-        m[0] = fmaxf(keep, __shfl_xor_sync(kFull, send, 2));
-    }
-    m[0] = fmaxf(m[0], __shfl_xor_sync(kFull, m[0], 16));
+    const float send = b0 ? m[0] : m[1], keep = b0 ? m[1] : m[0];
+    float a = fmaxf(keep, __shfl_xor_sync(kFull, send, 2));
+    a = fmaxf(a, __shfl_xor_sync(kFull, a, 16));
     float sc, inv;
-    group_scale<false>(m[0], sc, inv);
+    group_scale<false>(a, sc, inv);
     if (lane < 16) st[8 * (lane & 1) + (lane >> 1)] = sc;
-    ColScale r;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r.inv[j] = __shfl_sync(kFull, inv, 2 * j + (lane & 1));
-    return r;
+    for (int j = 0; j < 8; ++j) m[j] = __shfl_sync(kFull, inv, 2 * j + (lane & 1));
 }
 
+// n / d for n < 2^31 and the d that (mul, shift) were made for.
+struct FastDiv {
+    uint32_t mul, shift;
+};
+__device__ __forceinline__ uint32_t div_by(uint32_t n, FastDiv d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
+
+// A CTA's tiles, one after another: items of kColBlocks channel blocks of one group, every gridDim.x-th
+// in the order of the channel blocks, then the groups; `slot` counts the items modulo 3.
+constexpr uint32_t kColBlocks = 4;
+struct TileWalk {
+    uint32_t cb, first, g, slot, groups, CB, dcb, dg;
+    __device__ TileWalk(uint32_t n, uint32_t blocks)
+        : first(blockIdx.x / n * kColBlocks), g(blockIdx.x % n), slot(0), groups(n), CB(blocks),
+          dcb(gridDim.x / n * kColBlocks), dg(gridDim.x % n)
+    {
+        cb = first;
+    }
+    __device__ bool live() const { return cb < CB; }
+    __device__ bool at_first() const { return cb == first; }
+    __device__ void next_item()
+    {
+        first += dcb;
+        g += dg;
+        if (g >= groups) {
+            g -= groups;
+            first += kColBlocks;
+        }
+        cb = first;
+        slot = slot == 2 ? 0 : slot + 1;
+    }
+    __device__ void next()
+    {
+        if (++cb == first + kColBlocks || cb == CB) next_item();
+    }
+};
+
 template <bool WEIGHTED>
-__global__ void __launch_bounds__(256, WEIGHTED ? 2 : 3) moe_dispatch_cols_kernel(
+__global__ void __launch_bounds__(256, 3) moe_dispatch_cols_kernel(
     const uint16_t* __restrict__ x, const int32_t* __restrict__ slots, const float* __restrict__ weights,
-    const int32_t* __restrict__ offsets, int E, int64_t M, int k, uint32_t C, uint8_t* __restrict__ qt,
+    const int32_t* __restrict__ offsets, int E, int64_t M, FastDiv k, uint32_t C, uint8_t* __restrict__ qt,
     float* __restrict__ st, int64_t Kcap)
 {
     griddep_launch_dependents();
     griddep_wait();
-    __shared__ GroupTable table;
+    extern __shared__ __align__(16) uint8_t smem[];
+    int* s_token = reinterpret_cast<int*>(smem + 2 * kStageBytes);               // [3][128], -1: no row
+    float* s_weight = reinterpret_cast<float*>(smem + 2 * kStageBytes + 1536);   // [3][128]
+    const GroupTable table(smem + 2 * kStageBytes + 3072, E);
     if (!group_table(table, offsets, E, M, Kcap)) return;
-    const int lane = threadIdx.x & 31, r = lane >> 1, h = lane & 1;
-    const uint32_t groups = table.pre[E], tiles = groups * (C >> 7);
-    const uint32_t warps = (gridDim.x * blockDim.x) >> 5;
-    for (uint32_t tile = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; tile < tiles; tile += warps) {
-        const uint32_t cb = tile / groups, g = tile - cb * groups;
-        int64_t r0;
-        int nvalid;
-        group_rows(table, E, (int)g, r0, nvalid);
-        int token[8];
-        float wt[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            token[i] = -1;
-            wt[i] = 0.0f;
-            if (8 * r + i < nvalid) {
-                const int32_t slot = __ldg(slots + r0 + 8 * r + i);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, r = lane >> 1, h = lane & 1;
+    const uint32_t stage = smem_u32(smem);
+    TileWalk at(table.pre[E], C >> 7), ahead = at, later = at;   // this tile, the next one, an item to look up
+
+    // The token (and weight) of row `tid` of an item, for the threads that have one.
+    int token;
+    float weight;
+    auto look_up = [&]() {
+        token = -1;
+        weight = 0.0f;
+        if (tid < 128 && later.live()) {
+            int64_t r0;
+            int nvalid;
+            group_rows(table, E, (int)later.g, r0, nvalid);
+            if (tid < nvalid) {
+                const int32_t slot = __ldg(slots + r0 + tid);
                 if (slot >= 0 && slot < M) {
-                    token[i] = slot / k;
-                    if (WEIGHTED) wt[i] = __ldg(weights + slot);
+                    token = (int)div_by((uint32_t)slot, k);
+                    if (WEIGHTED) weight = __ldg(weights + slot);
                 } else {
                     latch_status(kDevBadIndex);
                 }
             }
         }
-        uint8_t* out = qt + (int64_t)(cb * 128 + 8 * h) * Kcap + (int64_t)g * 128 + 8 * r;
-        float* sc = st + (uint64_t)g * C + cb * 128;
-        const uint16_t* src = x + cb * 128 + 8 * h;
-#pragma unroll 1
-        for (int sl = 0; sl < kColSlices; ++sl, src += 16, out += 16 * Kcap, sc += 16) {
-            uint4 v[8];
+    };
+    auto note = [&]() {
+        if (tid < 128) {
+            s_token[128 * later.slot + tid] = token;
+            if (WEIGHTED) s_weight[128 * later.slot + tid] = weight;
+        }
+    };
+    // Copies of a tile's rows: half-warp (w, half) brings rows 16w + 8 half + i.
+    auto fetch = [&](const TileWalk& t, int buf) {
+        if (t.live()) {
+            const int row = 16 * w + 8 * (lane >> 4), c = lane & 15;
+            const int4 ta = *reinterpret_cast<const int4*>(s_token + 128 * t.slot + row);
+            const int4 tb = *reinterpret_cast<const int4*>(s_token + 128 * t.slot + row + 4);
+            const int n[8] = {ta.x, ta.y, ta.z, ta.w, tb.x, tb.y, tb.z, tb.w};
+            const uint16_t* src = x + t.cb * 128 + 8 * c;
+            const uint32_t dst = stage + buf * kStageBytes;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                copy16(dst + stage_at(row + i, c), src + (uint64_t)(uint32_t)max(n[i], 0) * C, n[i] >= 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    look_up();
+    note();
+    later.next_item();
+    look_up();
+    note();
+    later.next_item();
+    __syncthreads();
+    fetch(ahead, 0);
+    ahead.next();
+    // An item's tokens are looked up while the first tile of the item before the one before it is
+    // quantised, and noted at that tile's end: a barrier before the first copy that needs them, and after
+    // the last use of the three items older ones in that place.
+    for (int buf = 0; at.live(); at.next(), buf ^= 1) {
+        const uint32_t cb = at.cb, g = at.g;
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        float wt[8];
+        if (WEIGHTED) {
+            const float4 wa = *reinterpret_cast<const float4*>(s_weight + 128 * at.slot + 8 * r);
+            const float4 wb = *reinterpret_cast<const float4*>(s_weight + 128 * at.slot + 8 * r + 4);
+            wt[0] = wa.x; wt[1] = wa.y; wt[2] = wa.z; wt[3] = wa.w;
+            wt[4] = wb.x; wt[5] = wb.y; wt[6] = wb.z; wt[7] = wb.w;
+        }
+        __syncthreads();   // this tile has landed, and the other buffer is free
+        fetch(ahead, buf ^ 1);
+        ahead.next();
+        if (at.at_first()) look_up();
+
+        uint4 v[8];
+        const uint8_t* mine = smem + buf * kStageBytes + stage_at(8 * r, 2 * w + h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(mine + 256 * i);
+        float m[8];
+        if (WEIGHTED) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                m[2 * j] = m[2 * j + 1] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = mul2(widen(word(v[i], j)), make_float2(wt[i], wt[i]));
+                    m[2 * j] = fmaxf(m[2 * j], fabsf(f.x));
+                    m[2 * j + 1] = fmaxf(m[2 * j + 1], fabsf(f.y));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t p = 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p = maxabs2(p, word(v[i], j));
+                m[2 * j] = fabsf(bf16_lo(p));
+                m[2 * j + 1] = fabsf(bf16_hi(p));
+            }
+        }
+        column_scales(m, lane, st + (uint64_t)g * C + cb * 128 + 16 * w);
+        uint8_t* out = qt + (int64_t)(cb * 128 + 16 * w + 8 * h) * Kcap + (int64_t)g * 128 + 8 * r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {   // channels 8h + 2j, + 1
+            const float2 inv = make_float2(m[2 * j], m[2 * j + 1]);
+            float2 y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (token[i] >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(src + (uint64_t)(uint32_t)token[i] * C));
+                y[i] = widen(word(v[i], j));
+                if (WEIGHTED) y[i] = mul2(y[i], make_float2(wt[i], wt[i]));
+                y[i] = mul2(y[i], inv);
             }
-            float m[8];
-            float2 f[4][8];   // weighted: the products, formed once
-            if (WEIGHTED) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    m[2 * j] = m[2 * j + 1] = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t u = j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w;
-                        f[j][i] = mul2(widen(u), make_float2(wt[i], wt[i]));
-                        m[2 * j] = fmaxf(m[2 * j], fabsf(f[j][i].x));
-                        m[2 * j + 1] = fmaxf(m[2 * j + 1], fabsf(f[j][i].y));
-                    }
-                }
-            } else {
-                uint32_t p[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    p[0] = maxabs2(p[0], v[i].x);
-                    p[1] = maxabs2(p[1], v[i].y);
-                    p[2] = maxabs2(p[2], v[i].z);
-                    p[3] = maxabs2(p[3], v[i].w);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    m[2 * j] = fabsf(bf16_lo(p[j]));
-                    m[2 * j + 1] = fabsf(bf16_hi(p[j]));
-                }
-            }
-            const ColScale cs = column_scales(m, lane, sc);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {   // channels 8h + 2j, + 1
-                const float2 inv = make_float2(cs.inv[2 * j], cs.inv[2 * j + 1]);
-                float2 y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t u = j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w;
-                    y[i] = mul2(WEIGHTED ? f[j][i] : widen(u), inv);
-                }
-                *reinterpret_cast<uint2*>(out + (2 * j) * Kcap) =
-                    make_uint2(e4m3x2(y[0].x, y[1].x) | (e4m3x2(y[2].x, y[3].x) << 16),
-                               e4m3x2(y[4].x, y[5].x) | (e4m3x2(y[6].x, y[7].x) << 16));
-                *reinterpret_cast<uint2*>(out + (2 * j + 1) * Kcap) =
-                    make_uint2(e4m3x2(y[0].y, y[1].y) | (e4m3x2(y[2].y, y[3].y) << 16),
-                               e4m3x2(y[4].y, y[5].y) | (e4m3x2(y[6].y, y[7].y) << 16));
-            }
+            *reinterpret_cast<uint2*>(out) = make_uint2(codes4(y[0].x, y[1].x, y[2].x, y[3].x),
+                                                        codes4(y[4].x, y[5].x, y[6].x, y[7].x));
+            out += Kcap;
+            *reinterpret_cast<uint2*>(out) = make_uint2(codes4(y[0].y, y[1].y, y[2].y, y[3].y),
+                                                        codes4(y[4].y, y[5].y, y[6].y, y[7].y));
+            out += Kcap;
+        }
+        if (at.at_first()) {
+            note();
+            later.next_item();
         }
     }
 }
@@ -960,8 +1061,9 @@ __global__ void __launch_bounds__(256, 2) swiglu_backward_kernel(
 {
     griddep_launch_dependents();
     griddep_wait();
-    __shared__ GroupTable table;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) TileScratch sm;
+    const GroupTable table(smem, E);
     if (!group_table(table, offsets, E, M, Kcap)) return;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t IB = I >> 7, groups = table.pre[E], tiles = groups * IB;
