@@ -32,6 +32,33 @@ unsigned grid_for(int64_t items, int per_sm)
     return (unsigned)(items < n ? (items > 0 ? items : 1) : n);
 }
 
+// One cluster of `ctas` CTAs, in programmatic stream order as launch_kernel.
+template <typename... KArgs, typename... Args>
+int launch_cluster(void (*kern)(KArgs...), int ctas, dim3 block, size_t smem, cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return FP8Q_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+constexpr int64_t kPlanOneCta = 1024;
+
 template <typename L, bool SOFTMAX>
 int launch_route(const void* logits, const float* bias, int64_t T, int E, int k, int n_group, int topk_group,
                  int renorm, float scale, int32_t* idx, float* w, cudaStream_t st)
@@ -137,12 +164,13 @@ int fp8q_moe_plan(const int32_t* idx, int64_t T, int32_t k, int32_t E, int32_t* 
         const size_t bytes = (size_t)(E + 1) * sizeof(int32_t);
         return cudaMemsetAsync(offsets, 0, bytes, st) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
     }
-    const size_t smem = (size_t)E * kPlanWarps * sizeof(int32_t);
-    if (cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMoeMaxExperts * kPlanWarps * (int)sizeof(int32_t)) != cudaSuccess)
+    // One CTA does a few thousand slots faster than a cluster starts and meets.
+    const int ctas = T * k <= kPlanOneCta ? 1 : kPlanCtas;
+    const auto plan = ctas == 1 ? moe_plan_kernel<1> : moe_plan_kernel<kPlanCtas>;
+    if (cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_smem(kMoeMaxExperts)) != cudaSuccess)
         return FP8Q_ERR_CUDA;
-    return launch_kernel(moe_plan_kernel, dim3(1), dim3(kPlanThreads), smem, st, false, idx, T * k, (int)E, offsets,
-                         slots, rows);
+    return launch_cluster(plan, ctas, dim3(kPlanThreads), (size_t)plan_smem(E), st, idx, T * k, (int)E, offsets, slots,
+                          rows);
 }
 
 int fp8q_moe_dispatch(const uint16_t* x, const int32_t* offsets, const int32_t* slots, const int32_t* rows,
