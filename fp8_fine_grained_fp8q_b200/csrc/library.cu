@@ -65,9 +65,11 @@ int launch_route(const void* logits, const float* bias, int64_t T, int E, int k,
 {
     const dim3 grid((unsigned)((T + 3) / 4));
     const L* l = static_cast<const L*>(logits);
-#define FP8Q_ROUTE(NV)                                                                                              \
-    return launch_kernel(moe_route_kernel<L, NV, SOFTMAX>, grid, dim3(128), 0, st, false, l, bias, T, E, k, n_group, \
-                         topk_group, renorm, scale, idx, w)
+    const RouteShape sh{E, k, n_group, topk_group};
+    const bool wide = E % 8 == 0 && aligned16(logits) && aligned16(bias);
+#define FP8Q_ROUTE(NV)                                                                                             \
+    return launch_kernel(moe_route_kernel<L, NV, SOFTMAX>, grid, dim3(128), 0, st, false, l, bias, T, sh, wide, renorm, \
+                         scale, idx, w)
     if (E <= 32) FP8Q_ROUTE(1);
     if (E <= 64) FP8Q_ROUTE(2);
     if (E <= 128) FP8Q_ROUTE(4);

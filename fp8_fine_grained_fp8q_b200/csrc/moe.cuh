@@ -32,33 +32,6 @@ __device__ __forceinline__ uint32_t bf16_rn(float x)
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = (uint16_t)bf16_rn(v); }
 
-// ------------------------------------------------------------------------------------------
-// Routing.  One warp per token; lane l holds experts l, l + 32, ...  The order of the experts is
-// that of key = score + bias in binary64 (without a bias that of the logits themselves, which is
-// the same order and needs no arithmetic); equal keys go to the lower index.  A masked expert
-// (logit or bias -inf, NaN or +inf) has the key -inf.
-// ------------------------------------------------------------------------------------------
-struct Ranked {
-    double key;
-    int e;
-};
-__device__ __forceinline__ bool before(double ka, int ea, double kb, int eb)
-{
-    return ka > kb || (ka == kb && ea < eb);
-}
-__device__ __forceinline__ Ranked warp_first(Ranked r)
-{
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        const double k = __shfl_xor_sync(kFull, r.key, o);
-        const int e = __shfl_xor_sync(kFull, r.e, o);
-        if (before(k, e, r.key, r.e)) {
-            r.key = k;
-            r.e = e;
-        }
-    }
-    return r;
-}
 __device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll
@@ -73,133 +46,324 @@ __device__ __forceinline__ T warp_sum(T v)
     return v;
 }
 
+// ------------------------------------------------------------------------------------------
+// Routing.  One warp per token; lane l holds the NV consecutive experts l NV ..  The order of the
+// experts is that of key = score + bias in binary64 (without a bias that of the logits themselves,
+// which is the same order and needs no arithmetic); equal keys go to the lower index.  A masked
+// expert (logit or bias -inf, NaN or +inf) has the key -inf.
+//
+// Keys are first formed in binary32, whose error is bounded below.  Where two neighbours in the order
+// found that way (or the groups on the two sides of the border) are nearer than the bound, the token is
+// done again with keys in binary64; that is rare, and it costs the few tokens about 3 us.  With
+// binary64 throughout, 8192 tokens of 256 experts took 65 us instead of 11.
+// Bound by latency and instruction issue; the logits are 8 MB.
+// ------------------------------------------------------------------------------------------
+// Keys as unsigned integers of the same order, above 1.  0: not to be chosen (again); 1: masked.
+__device__ __forceinline__ uint32_t rank_of(float f)
+{
+    const uint32_t u = __float_as_uint(f + 0.0f);   // -0 is 0
+    return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ unsigned long long rank_of(double f)
+{
+    const unsigned long long u = (unsigned long long)__double_as_longlong(f + 0.0);
+    return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+}
+__device__ __forceinline__ uint32_t warp_top(uint32_t v) { return __reduce_max_sync(kFull, v); }
+__device__ __forceinline__ unsigned long long warp_top(unsigned long long v)
+{
+    const uint32_t hi = __reduce_max_sync(kFull, (uint32_t)(v >> 32));
+    const uint32_t lo = __reduce_max_sync(kFull, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+    return ((unsigned long long)hi << 32) | lo;
+}
+template <typename F> struct Rank { typedef uint32_t type; };
+template <> struct Rank<double> { typedef unsigned long long type; };
+template <typename F> __device__ __forceinline__ F lowest() { return (F)-CUDART_INF_F; }
+
+// (a, b) <- the two largest of a, b, c, d with a >= b, c >= d.
+template <typename F>
+__device__ __forceinline__ void merge_two(F& a, F& b, F c, F d)
+{
+    b = a > c ? (b > c ? b : c) : (a > d ? a : d);
+    a = a > c ? a : c;
+}
+
+struct RouteShape {
+    int E, k, n_group, topk_group;
+};
+
+// Lane j: the j-th expert by key[i] (of expert lane * NV + i; -inf: masked).  `pair`: a group's score is
+// the sum of its two largest keys, not its largest.  near, near_group: where the keys of two neighbours
+// (the scores of the groups at the border) are not further apart, and not from the same logit and bias,
+// *unsure is set; negative: the keys are exact.
+template <typename F, int NV, typename Same>
+__device__ __forceinline__ int choose(const F (&key)[NV], const RouteShape& sh, bool pair, F near, F near_group,
+                                      Same same, bool* unsure)
+{
+    typedef typename Rank<F>::type R;
+    const int lane = threadIdx.x & 31, e0 = lane * NV;
+    const int per = sh.E / sh.n_group;
+    uint32_t allowed = kFull;   // bit g: experts of group g may be chosen
+    if (sh.n_group > sh.topk_group) {
+        F mine = lowest<F>();   // lane g: the score of group g
+        const int seg = per / NV;
+        if (seg * NV == per && (seg & (seg - 1)) == 0) {
+            // A group is a power of two of whole lanes: the two largest by a butterfly in each.
+            F a = lowest<F>(), b = lowest<F>();
+#pragma unroll
+            for (int i = 0; i < NV; ++i) merge_two(a, b, key[i], lowest<F>());
+            for (int o = 1; o < seg; o <<= 1) merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
+            mine = __shfl_sync(kFull, pair && b > lowest<F>() ? a + b : a, (lane * seg) & 31);
+        } else {
+            for (int g = 0; g < sh.n_group; ++g) {
+                F a = lowest<F>(), b = lowest<F>();
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (e0 + i >= g * per && e0 + i < (g + 1) * per) merge_two(a, b, key[i], lowest<F>());
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1)
+                    merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
+                if (lane == g) mine = pair && b > lowest<F>() ? a + b : a;
+            }
+        }
+        int rank = 0;
+        for (int g = 0; g < sh.n_group; ++g) {
+            const F other = __shfl_sync(kFull, mine, g);
+            if (other > mine || (other == mine && g < lane)) ++rank;
+        }
+        if (lane >= sh.n_group) rank = 32;
+        allowed = __ballot_sync(kFull, rank < sh.topk_group);
+        if (pair && near_group >= (F)0) {
+            const F in = __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, rank == sh.topk_group - 1)) - 1);
+            const F out = __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, rank == sh.topk_group)) - 1);
+            if (out > lowest<F>() && !(in - out > near_group)) *unsure = true;
+        }
+    }
+    R rank[NV];
+    int g = e0 / per, left = per - (e0 - g * per);   // the group at hand, and its experts from here on
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (left == 0) {
+            left = per;
+            ++g;
+        }
+        --left;
+        rank[i] = key[i] > lowest<F>() ? rank_of(key[i]) : (R)1;
+        if (e0 + i >= sh.E || !((allowed >> (g & 31)) & 1u)) rank[i] = 0;
+    }
+    R best = 0;   // of this lane
+#pragma unroll
+    for (int i = 0; i < NV; ++i) best = best > rank[i] ? best : rank[i];
+    int chosen = 0, last_e = -1;
+    F last = lowest<F>();
+    const bool check = near >= (F)0;
+    const int rounds = check && sh.topk_group * per > sh.k ? sh.k + 1 : sh.k;
+    for (int j = 0; j < rounds; ++j) {
+        const R top = warp_top(best);
+        const int who = __ffs(__ballot_sync(kFull, best == top)) - 1;   // the lowest lane has the lowest index
+        int at = 0;
+        F value = lowest<F>();
+        if (lane == who) {
+#pragma unroll
+            for (int i = NV - 1; i >= 0; --i)
+                if (rank[i] == top) {
+                    at = i;
+                    value = key[i];
+                }
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i == at) rank[i] = 0;
+                best = best > rank[i] ? best : rank[i];
+            }
+        }
+        const int e = __shfl_sync(kFull, e0 + at, who);
+        if (check) {
+            value = __shfl_sync(kFull, value, who);
+            if (j > 0 && value > lowest<F>() && !(last - value > near)) {
+                // Equal inputs have equal keys; at the border an equal neighbour may hide the next one.
+                if (j == sh.k || !same(last_e, e)) *unsure = true;
+            }
+            last = value;
+            last_e = e;
+        }
+        if (lane == j) chosen = e;   // (round k is for the check only)
+    }
+    return chosen;
+}
+
+template <typename L, int NV>
+struct RouteRow {
+    float l[NV];   // usable logits; -inf for the others
+    float b[NV];   // usable biases; -inf for the others
+    float top;     // the largest usable logit
+    bool bad;      // a NaN or +inf somewhere in the row or the bias
+};
+
+// NV consecutive values from p, whole 16-byte loads where `wide`.
+template <int NV>
+__device__ __forceinline__ void load_some(const float* p, int n, bool wide, float (&v)[NV])
+{
+    if (NV % 4 == 0 && wide) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+            float4 f = make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+            if (i < n) f = __ldg(reinterpret_cast<const float4*>(p + i));
+            v[i] = f.x;
+            v[(i + 1) % NV] = f.y;
+            v[(i + 2) % NV] = f.z;
+            v[(i + 3) % NV] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = i < n ? __ldg(p + i) : -CUDART_INF_F;
+    }
+}
+template <int NV>
+__device__ __forceinline__ void load_some(const uint16_t* p, int n, bool wide, float (&v)[NV])
+{
+    if (NV % 8 == 0 && wide) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 8) {
+            uint4 f = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);   // -inf
+            if (i < n) f = __ldg(reinterpret_cast<const uint4*>(p + i));
+            const uint32_t u[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[(i + 2 * j) % NV] = __uint_as_float(u[j] << 16);
+                v[(i + 2 * j + 1) % NV] = __uint_as_float(u[j] & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = i < n ? __uint_as_float((uint32_t)__ldg(p + i) << 16) : -CUDART_INF_F;
+    }
+}
+
+// wide: E is a multiple of 8 and the rows are 16-byte aligned (then a lane's experts are too, and
+// each 16-byte piece lies inside the row or outside it).
+template <typename L, int NV>
+__device__ __forceinline__ void load_route(RouteRow<L, NV>& r, const L* row, const float* bias, int E, bool wide)
+{
+    const int e0 = (threadIdx.x & 31) * NV;
+    load_some<NV>(row + e0, E - e0, wide, r.l);
+    if (bias) {
+        load_some<NV>(bias + e0, E - e0, wide, r.b);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) r.b[i] = 0.0f;
+    }
+    bool bad = false;
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        bad |= !(r.l[i] < CUDART_INF_F) || !(r.b[i] < CUDART_INF_F);
+        if (!(r.l[i] < CUDART_INF_F)) r.l[i] = -CUDART_INF_F;
+        if (!(r.b[i] < CUDART_INF_F)) r.b[i] = -CUDART_INF_F;
+        top = fmaxf(top, r.l[i]);
+    }
+    r.bad = __any_sync(kFull, bad);
+    r.top = warp_max(top);
+}
+
+// The choice with keys in binary64; only ever with a bias.
+template <typename L, int NV, bool SOFTMAX>
+__device__ __noinline__ int choose_exactly(const L* row, const float* bias, RouteShape sh, bool wide)
+{
+    RouteRow<L, NV> r;
+    load_route<L, NV>(r, row, bias, sh.E, wide);
+    double key[NV], total = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        key[i] = 0.0;
+        if (r.l[i] > -CUDART_INF_F) key[i] = SOFTMAX ? exp((double)r.l[i] - (double)r.top) : 1.0 / (1.0 + exp(-(double)r.l[i]));
+        total += key[i];
+    }
+    if (SOFTMAX) total = warp_sum(total);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (SOFTMAX) key[i] = key[i] / total;
+        key[i] = r.l[i] > -CUDART_INF_F && r.b[i] > -CUDART_INF_F ? key[i] + (double)r.b[i] : -CUDART_INF;
+    }
+    bool unsure = false;
+    return choose<double, NV>(key, sh, true, -1.0, -1.0, [](int, int) { return true; }, &unsure);
+}
+
 template <typename L, int NV, bool SOFTMAX>
 __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ logits, const float* __restrict__ bias,
-                                                        int64_t T, int E, int k, int n_group, int topk_group,
-                                                        int renorm, float scale, int32_t* __restrict__ idx,
-                                                        float* __restrict__ w)
+                                                        int64_t T, RouteShape sh, bool wide, int renorm, float scale,
+                                                        int32_t* __restrict__ idx, float* __restrict__ w)
 {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (t >= T) return;
-    const L* row = logits + t * E;
-    const int per = E / n_group;
+    const L* row = logits + t * sh.E;
+    RouteRow<L, NV> r;
+    load_route<L, NV>(r, row, bias, sh.E, wide);
 
-    float l[NV];
-    bool bad = false;
-    float top = -CUDART_INF_F;   // the largest usable logit
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = -CUDART_INF_F;
-        if (e < E) {
-            const float x = load_logit(row + e);
-            const float b = bias ? bias[e] : 0.0f;
-            bad |= !(x < CUDART_INF_F) || !(b < CUDART_INF_F);
-            if (x < CUDART_INF_F) l[i] = x;
-        }
-        top = fmaxf(top, l[i]);
-    }
-    bad = __any_sync(kFull, bad);
-    top = warp_max(top);
-    double total = 1.0;
-    if (SOFTMAX) {
-        total = 0.0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (l[i] > -CUDART_INF_F) total += exp((double)l[i] - (double)top);
-        total = warp_sum(total);
-    }
-
-    double key[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = -CUDART_INF;
-        if (e < E && l[i] > -CUDART_INF_F) {
-            if (bias) {
-                const float b = bias[e];
-                const double s = SOFTMAX ? exp((double)l[i] - (double)top) / total : 1.0 / (1.0 + exp(-(double)l[i]));
-                if (b > -CUDART_INF_F && b < CUDART_INF_F) key[i] = s + (double)b;
-            } else {
-                key[i] = (double)l[i];
-            }
-        }
-    }
-
-    uint32_t allowed = kFull;   // bit g: experts of group g may be chosen
-    if (n_group > 1) {
-        double mine = -CUDART_INF;   // lane g: the score of group g
-        for (int g = 0; g < n_group; ++g) {
-            Ranked r1{-CUDART_INF, 0x7FFFFFFF}, r2{-CUDART_INF, 0x7FFFFFFF};
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int e = lane + 32 * i;
-                if (e / per == g && before(key[i], e, r1.key, r1.e)) r1 = Ranked{key[i], e};
-            }
-            r1 = warp_first(r1);
-            double score = r1.key;
-            if (bias) {   // the sum of the two largest keys (of the one there is)
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e / per == g && e != r1.e && before(key[i], e, r2.key, r2.e)) r2 = Ranked{key[i], e};
-                }
-                r2 = warp_first(r2);
-                if (r2.key > -CUDART_INF) score += r2.key;
-            }
-            if (lane == g) mine = score;
-        }
-        int rank = 0;
-        for (int g = 0; g < n_group; ++g) {
-            const double other = __shfl_sync(kFull, mine, g);
-            if (before(other, g, mine, lane)) ++rank;
-        }
-        allowed = __ballot_sync(kFull, lane < n_group && rank < topk_group);
-    }
-
-    uint32_t taken = 0u;
-    int chosen = 0;   // lane j: the j-th expert
-    for (int j = 0; j < k; ++j) {
-        Ranked r{-CUDART_INF, 0x7FFFFFFF};
+    // Scores.  e^x by __expf is off by (2 + 1.2 |x|) 2^-23 of itself, so sigmoid by less than 2^-22 in all
+    // (s (1 - s) (2 + 1.2 |l|) < 0.65), and softmax, whose sum of up to 1024 terms adds 37 roundings, by
+    // less than 2^-18.  A key's own rounding is 2^-24 of it.  `near` is twice the sum of two such errors.
+    float total = 0.0f, key[NV];
+    if (SOFTMAX || bias) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = lane + 32 * i;
-            if (e < E && !((taken >> i) & 1u) && ((allowed >> (e / per)) & 1u) && before(key[i], e, r.key, r.e))
-                r = Ranked{key[i], e};
+            key[i] = 0.0f;
+            if (r.l[i] > -CUDART_INF_F)
+                key[i] = SOFTMAX ? __expf(r.l[i] - r.top) : __fdividef(1.0f, 1.0f + __expf(-r.l[i]));
+            total += key[i];
         }
-        r = warp_first(r);
-        if ((r.e & 31) == lane) taken |= 1u << (r.e >> 5);
-        if (lane == j) chosen = r.e;
+        if (SOFTMAX) total = warp_sum(total);
+    }
+    int chosen;
+    if (!bias) {
+        bool unsure = false;
+        chosen = choose<float, NV>(r.l, sh, false, -1.0f, -1.0f, [](int, int) { return true; }, &unsure);
+    } else {
+        float largest = 0.0f;
+        const float inv = SOFTMAX ? __fdividef(1.0f, total) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool usable = r.l[i] > -CUDART_INF_F && r.b[i] > -CUDART_INF_F;
+            key[i] = usable ? (SOFTMAX ? key[i] * inv : key[i]) + r.b[i] : -CUDART_INF_F;
+            if (usable) largest = fmaxf(largest, fabsf(key[i]));
+        }
+        largest = warp_max(largest);
+        const float near = (SOFTMAX ? 0x1p-16f : 0x1p-20f) + 0x1p-22f * largest;
+        bool unsure = false;
+        chosen = choose<float, NV>(key, sh, true, near, 4.0f * near,
+                                   [&](int p, int q) { return load_logit(row + p) == load_logit(row + q) && bias[p] == bias[q]; },
+                                   &unsure);
+        if (unsure) chosen = choose_exactly<L, NV, SOFTMAX>(row, bias, sh, wide);   // the same for the whole warp
     }
 
     // Weights.  The renormalised ones divide scores by their sum, so scores that would underflow are
     // first scaled by exp(-m), m = min(largest chosen logit, 0): sigmoid(l) e^-m = e^(l-m) / (1 + e^l).
     bool usable = false;
     float x = -CUDART_INF_F;
-    if (lane < k) {
+    if (lane < sh.k) {
         x = load_logit(row + chosen);
         const float b = bias ? bias[chosen] : 0.0f;
         usable = x > -CUDART_INF_F && x < CUDART_INF_F && b > -CUDART_INF_F && b < CUDART_INF_F;
     }
     const float best = warp_max(usable ? x : -CUDART_INF_F);
-    double s = 0.0;
+    float s = 0.0f;
     if (usable) {
-        const double m = renorm ? (SOFTMAX ? (double)best : fmin((double)best, 0.0)) : 0.0;
+        const float m = renorm ? (SOFTMAX ? best : fminf(best, 0.0f)) : 0.0f;
         if (SOFTMAX)
-            s = renorm ? exp((double)x - m) : exp((double)x - (double)top) / total;
+            s = renorm ? expf(x - m) : expf(x - r.top) / total;
         else
-            s = x > 0.0f ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - m) / (1.0 + exp((double)x));
+            s = x > 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - m) / (1.0f + expf(x));
     }
     if (renorm) {
-        const double sum = warp_sum(s);
-        s = sum > 0.0 ? s / sum : 0.0;
+        const float sum = warp_sum(s);
+        s = sum > 0.0f ? s / sum : 0.0f;
     }
-    if (lane < k) {
-        idx[t * k + lane] = chosen;
-        w[t * k + lane] = bad ? CUDART_NAN_F : (float)(s * (double)scale);
+    if (lane < sh.k) {
+        idx[t * sh.k + lane] = chosen;
+        w[t * sh.k + lane] = r.bad ? CUDART_NAN_F : s * scale;
     }
 }
 
