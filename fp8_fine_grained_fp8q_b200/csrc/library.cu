@@ -59,6 +59,21 @@ int launch_cluster(void (*kern)(KArgs...), int ctas, dim3 block, size_t smem, cu
 
 constexpr int64_t kPlanOneCta = 1024;
 
+// Lets a kernel have up to `bytes` of dynamic shared memory, once a device (`ready`: the kernel's own).
+template <typename Kernel>
+bool allow_smem(Kernel kern, int bytes, std::atomic<bool> (&ready)[kMaxDevices])
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    if (ready[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    ready[dev].store(true, std::memory_order_release);
+    return true;
+}
+
 template <typename L, bool SOFTMAX>
 int launch_route(const void* logits, const float* bias, int64_t T, int E, int k, int n_group, int topk_group,
                  int renorm, float scale, int32_t* idx, float* w, cudaStream_t st)
@@ -169,8 +184,8 @@ int fp8q_moe_plan(const int32_t* idx, int64_t T, int32_t k, int32_t E, int32_t* 
     // One CTA does a few thousand slots faster than a cluster starts and meets.
     const int ctas = T * k <= kPlanOneCta ? 1 : kPlanCtas;
     const auto plan = ctas == 1 ? moe_plan_kernel<1> : moe_plan_kernel<kPlanCtas>;
-    if (cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_smem(kMoeMaxExperts)) != cudaSuccess)
-        return FP8Q_ERR_CUDA;
+    static std::atomic<bool> ready[2][kMaxDevices];
+    if (!allow_smem(plan, plan_smem(kMoeMaxExperts), ready[ctas == 1])) return FP8Q_ERR_CUDA;
     return launch_cluster(plan, ctas, dim3(kPlanThreads), (size_t)plan_smem(E), st, idx, T * k, (int)E, offsets, slots,
                           rows);
 }
@@ -197,9 +212,8 @@ int fp8q_moe_dispatch(const uint16_t* x, const int32_t* offsets, const int32_t* 
     if (done != FP8Q_OK || !qt) return done;
     const int64_t items = ((M + 127) / 128 + E) * ((C / 128 + kColBlocks - 1) / kColBlocks);
     const auto by_column = weights ? moe_dispatch_cols_kernel<true> : moe_dispatch_cols_kernel<false>;
-    if (cudaFuncSetAttribute(by_column, cudaFuncAttributeMaxDynamicSharedMemorySize, gather_smem(kMoeMaxExperts)) !=
-        cudaSuccess)
-        return FP8Q_ERR_CUDA;
+    static std::atomic<bool> ready[2][kMaxDevices];
+    if (!allow_smem(by_column, gather_smem(kMoeMaxExperts), ready[weights != nullptr])) return FP8Q_ERR_CUDA;
     return launch_kernel(by_column, dim3(grid_for(items, 3)), dim3(256), gather_smem(E), cs, false, x, slots, weights,
                          offsets, (int)E, M, fast_div((uint32_t)k), (uint32_t)C, qt, st, Kcap);
 }

@@ -116,7 +116,7 @@ def _require(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int):
 
 def _out(t, shape, dtype, device, name):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     _require(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -445,14 +445,23 @@ class MoePlan(NamedTuple):
     rows: torch.Tensor      # int32 [T, k]
 
 
+def _at(t):
+    """A tensor's address, 0 for none."""
+    return 0 if t is None else t.data_ptr()
+
+
 def _launch(entry: str, dev: torch.device, *args):
-    """Call an entry point with `dev` current, on its current stream, and check the status."""
-    if torch.cuda.current_device() == dev.index:
-        status = getattr(lib(), entry)(*args, _stream(dev))
+    """Call an entry point with `dev` current, on its current stream, and check the status.  (The raw
+    stream: making torch's stream object takes 2 of the 11 us that a call otherwise costs the host.)"""
+    index = dev.index
+    fn = getattr(lib(), entry)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib(), entry)(*args, _stream(dev))
-    _check(entry, status)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        raise Fp8qError(entry, status)
 
 
 def _together(dev: torch.device, *named):
@@ -513,8 +522,8 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None
     idx = _out(idx, (T, top_k), torch.int32, dev, "idx")
     w = _out(w, (T, top_k), torch.float32, dev, "w")
     _together(dev, (bias, "bias"), (idx, "idx"), (w, "w"))
-    _launch("fp8q_moe_route", dev, _p(logits), kind, _p(bias), T, E, top_k, n_group, topk_group, fn,
-            int(renormalize), scale, _p(idx), _p(w))
+    _launch("fp8q_moe_route", dev, _at(logits), kind, _at(bias), T, E, top_k, n_group, topk_group, fn,
+            int(renormalize), scale, _at(idx), _at(w))
     return idx, w
 
 
@@ -534,8 +543,8 @@ def moe_route_backward(dw: torch.Tensor, w: torch.Tensor, idx: torch.Tensor, log
             raise ValueError(f"{name} must have shape {(T, k)}, got {tuple(t.shape)}")
     out = _out(out, (T, E), logits.dtype, dev, "out")
     _together(dev, (dw, "dw"), (w, "w"), (idx, "idx"), (out, "out"))
-    _launch("fp8q_moe_route_backward", dev, _p(dw), _p(w), _p(idx), _p(logits), kind, T, E, k, fn,
-            int(renormalize), scale, _p(out))
+    _launch("fp8q_moe_route_backward", dev, _at(dw), _at(w), _at(idx), _at(logits), kind, T, E, k, fn,
+            int(renormalize), scale, _at(out))
     return out
 
 
@@ -550,7 +559,7 @@ def moe_plan(idx: torch.Tensor, E: int, offsets: torch.Tensor | None = None, slo
     slots = _out(slots, (T * k,), torch.int32, dev, "slots")
     rows = _out(rows, (T, k), torch.int32, dev, "rows")
     _together(dev, (offsets, "offsets"), (slots, "slots"), (rows, "rows"))
-    _launch("fp8q_moe_plan", dev, _p(idx), T, k, E, _p(offsets), _p(slots), _p(rows))
+    _launch("fp8q_moe_plan", dev, _at(idx), T, k, E, _at(offsets), _at(slots), _at(rows))
     return MoePlan(offsets, slots, rows)
 
 
@@ -576,8 +585,8 @@ def moe_dispatch(x: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None = 
         qt = _out(qt, (C, Kcap), torch.uint8, dev, "qt")
         st = _out(st, (Kcap // 128, C), torch.float32, dev, "st")
     _together(dev, (q, "q"), (s, "s"), (qt, "qt"), (st, "st"))
-    _launch("fp8q_moe_dispatch", dev, _p(x), _p(plan.offsets), _p(plan.slots), _p(plan.rows), _p(weights), E, T, k, C,
-            _p(q), _p(s), _p(qt), _p(st), Kcap or 0)
+    _launch("fp8q_moe_dispatch", dev, _at(x), _at(plan.offsets), _at(plan.slots), _at(plan.rows), _at(weights), E, T, k, C,
+            _at(q), _at(s), _at(qt), _at(st), Kcap or 0)
     return q, s, qt, st
 
 
@@ -596,7 +605,7 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None = N
         add = _out(add, (T, C), torch.bfloat16, dev, "add")
     out = _out(out, (T, C), torch.bfloat16, dev, "out")
     _together(dev, (add, "add"), (out, "out"))
-    _launch("fp8q_moe_combine", dev, _p(y), _p(plan.rows), _p(weights), _p(add), T, k, C, _p(out))
+    _launch("fp8q_moe_combine", dev, _at(y), _at(plan.rows), _at(weights), _at(add), T, k, C, _at(out))
     return out
 
 
@@ -611,7 +620,7 @@ def moe_combine_dweight(dout: torch.Tensor, y: torch.Tensor, plan: MoePlan, out:
         raise ValueError(f"dout must be [{T}, C] and y [{T * k}, C], got {tuple(dout.shape)} and {tuple(y.shape)}")
     out = _out(out, (T, k), torch.float32, dev, "out")
     _together(dev, (y, "y"), (out, "out"))
-    _launch("fp8q_moe_combine_dweight", dev, _p(dout), _p(y), _p(plan.rows), T, k, C, _p(out))
+    _launch("fp8q_moe_combine_dweight", dev, _at(dout), _at(y), _at(plan.rows), T, k, C, _at(out))
     return out
 
 
@@ -632,7 +641,7 @@ def swiglu_quant(h: torch.Tensor, checkpoint: bool = True, q: torch.Tensor | Non
         hq = _out(hq, (M, two), torch.uint8, dev, "hq")
         hs = _out(hs, (two // 128, M), torch.float32, dev, "hs")
     _together(dev, (q, "q"), (s, "s"), (hq, "hq"), (hs, "hs"))
-    _launch("fp8q_swiglu_quant", dev, _p(h), M, I, _p(q), _p(s), _p(hq), _p(hs))
+    _launch("fp8q_swiglu_quant", dev, _at(h), M, I, _at(q), _at(s), _at(hq), _at(hs))
     return q, s, hq, hs
 
 
@@ -667,8 +676,8 @@ def swiglu_backward_quant(da: torch.Tensor, hq: torch.Tensor, hs: torch.Tensor, 
     ast = _out(ast, (Kcap // 128, I), torch.float32, dev, "ast")
     _together(dev, (hq, "hq"), (hs, "hs"), (offsets, "offsets"), (q, "q"), (s, "s"), (qt, "qt"), (st, "st"),
               (aqt, "aqt"), (ast, "ast"))
-    _launch("fp8q_swiglu_backward_quant", dev, _p(da), _p(hq), _p(hs), _p(offsets), E, M, I, _p(q), _p(s), _p(qt),
-            _p(st), _p(aqt), _p(ast), Kcap)
+    _launch("fp8q_swiglu_backward_quant", dev, _at(da), _at(hq), _at(hs), _at(offsets), E, M, I, _at(q), _at(s), _at(qt),
+            _at(st), _at(aqt), _at(ast), Kcap)
     return q, s, qt, st, aqt, ast
 
 
