@@ -254,8 +254,14 @@ int fp8q_swiglu_quant(const uint16_t* h, int64_t M, int64_t I, uint8_t* q, float
     if (M > kI32 || I > kI32 / 2) return FP8Q_ERR_UNSUPPORTED;
     if (!h || !q || !s || (hq == nullptr) != (hs == nullptr)) return FP8Q_ERR_ARG;
     if (!aligned16(h) || !aligned16(q) || !aligned16(s) || !aligned16(hq) || !aligned16(hs)) return FP8Q_ERR_ALIGN;
-    return launch_kernel(swiglu_quant_kernel, dim3(grid_for((M * (I / 128) + 31) / 32, 8)), dim3(256), 0,
-                         (cudaStream_t)stream, false, h, M, I, q, s, hq, hs);
+    // Eight rows a warp, unless that leaves SMs without a warp: then one.
+    const int64_t quads = (I / 128 + 3) / 4;
+    const int64_t rows = (M + 7) / 8 * quads >= 8 * (int64_t)grid_for(kI32, 4) ? 8 : 1;
+    const int64_t items = (M + rows - 1) / rows * quads;
+    if (items > kI32) return FP8Q_ERR_UNSUPPORTED;
+    const auto kern = hq ? swiglu_quant_kernel<true> : swiglu_quant_kernel<false>;
+    return launch_kernel(kern, dim3(grid_for((items + 7) / 8, 4)), dim3(256), 0, (cudaStream_t)stream, false, h,
+                         (uint32_t)M, (uint32_t)I, (uint32_t)rows, q, s, hq, hs);
 }
 
 int fp8q_swiglu_backward_quant(const uint16_t* da, const uint8_t* hq, const float* hs, const int32_t* offsets,

@@ -831,12 +831,16 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* 
             }
         } else {
             const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            float sc8 = 0.0f, inv8 = 0.0f;   // lane sub: of copy (j & ~7) + sub
             for (uint32_t j = 0; j < k; ++j) {
                 const int32_t r = __shfl_sync(kFull, row, j);
                 const float wj = __shfl_sync(kFull, wt, j);
                 // |w| max|x| is the largest |w x|: rounding keeps the order.
-                float sc, inv;
-                group_scale<false>(__fmul_rn(fabsf(wj), amax), sc, inv);
+                if ((j & 7) == 0) {
+                    const float w8 = __shfl_sync(kFull, wt, j + sub);
+                    group_scale<false>(__fmul_rn(fabsf(w8), amax), sc8, inv8);
+                }
+                const float sc = __shfl_sync(kFull, sc8, j & 7, 8), inv = __shfl_sync(kFull, inv8, j & 7, 8);
                 if (r < 0 || !live) continue;
                 uint32_t c[4];
 #pragma unroll
@@ -1250,47 +1254,86 @@ __global__ void __launch_bounds__(256) moe_combine_dweight_kernel(const uint16_t
 // ------------------------------------------------------------------------------------------
 // SwiGLU: a = silu(g) u with g = h[:, :I], u = h[:, I:], quantised from FP32; with `hq`, the 1x128
 // codes of h itself are the checkpoint that the backward pass starts from.  Eight lanes own one
-// 128-element tile of a (and the two tiles of h it comes from).
+// 128-element tile of a (and the two tiles of h that it comes from), a warp four neighbouring tiles of
+// `rows` rows, one row after another: with eight rows, the scales of a tile column leave as whole
+// 32-byte sectors.  One lane of the eight forms each of the three scales.
+// Bound by HBM; the two MUFU operations an element take 60 us of 65536 x 2048, the bytes 145.
 // ------------------------------------------------------------------------------------------
-__device__ __forceinline__ float sigmoidf(float x) { return 1.0f / (1.0f + expf(-x)); }
+// sigmoid by ex2 and a fast reciprocal: relative error below (4 + 1.2 |x|) 2^-23; x = -inf gives 0, and
+// beyond |x| = 88 the result is 0 or 1 as binary32 has it.
+__device__ __forceinline__ float sigmoidf(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
-__global__ void __launch_bounds__(256) swiglu_quant_kernel(const uint16_t* __restrict__ h, int64_t M, int64_t I,
-                                                           uint8_t* __restrict__ q, float* __restrict__ s,
-                                                           uint8_t* __restrict__ hq, float* __restrict__ hs)
+template <bool CKPT>
+__global__ void __launch_bounds__(256, 4) swiglu_quant_kernel(const uint16_t* __restrict__ h, uint32_t M, uint32_t I,
+                                                              uint32_t rows, uint8_t* __restrict__ q,
+                                                              float* __restrict__ s, uint8_t* __restrict__ hq,
+                                                              float* __restrict__ hs)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t IB = I >> 7, tiles = M * IB;
-    const int sub = threadIdx.x & 7;
-    const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 3;
-    const int64_t first = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
-    for (int64_t b = first - (first & 3); b < tiles; b += step) {
-        const int64_t i = b + (first & 3);
-        const bool live = i < tiles;
-        const int64_t m = live ? i / IB : 0, ib = live ? i - m * IB : 0;
-        const uint4* p = reinterpret_cast<const uint4*>(h + m * 2 * I + ib * 128) + 2 * sub;
-        const uint4* pu = reinterpret_cast<const uint4*>(h + m * 2 * I + I + ib * 128) + 2 * sub;
-        float g[16], u[16], a[16];
-        unpack16(__ldg(p), __ldg(p + 1), g);
-        unpack16(__ldg(pu), __ldg(pu + 1), u);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) a[j] = g[j] * sigmoidf(g[j]) * u[j];
-        float sc, inv;
-        group_scale<false>(max8(amax16f(a)), sc, inv);
-        if (live) {
-            reinterpret_cast<uint4*>(q + m * I + ib * 128)[sub] = quant16f(a, inv);
-            if (sub == 0) s[ib * M + m] = sc;
-        }
-        if (hq) {
-            group_scale<false>(max8(amax16f(g)), sc, inv);
+    const uint32_t IB = I >> 7, quads = (IB + 3) >> 2, bands = (M + rows - 1) / rows, items = bands * quads;
+    const uint32_t lane = threadIdx.x & 31, sub = lane & 7;
+    const uint32_t warps = (gridDim.x * blockDim.x) >> 5;
+    for (uint32_t it = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items; it += warps) {
+        const uint32_t band = it / quads, ib = (it - band * quads) * 4 + (lane >> 3);
+        const bool live = ib < IB;
+        const uint32_t m0 = band * rows, n = min(rows, M - m0);
+        const uint16_t* src = h + (size_t)m0 * 2 * I + ib * 128 + 16 * sub;
+        uint8_t* qa = q + (size_t)m0 * I + ib * 128 + 16 * sub;
+        uint8_t* qh = CKPT ? hq + (size_t)m0 * 2 * I + ib * 128 + 16 * sub : nullptr;
+        float sa = 0.0f, sg = 0.0f, su = 0.0f;   // lane sub: the scales of row m0 + sub
+        for (uint32_t i = 0; i < n; ++i, src += 2 * I, qa += I, qh += CKPT ? 2 * I : 0) {
+            uint4 g0 = make_uint4(0u, 0u, 0u, 0u), g1 = g0, u0 = g0, u1 = g0;
             if (live) {
-                reinterpret_cast<uint4*>(hq + m * 2 * I + ib * 128)[sub] = quant16f(g, inv);
-                if (sub == 0) hs[ib * M + m] = sc;
+                g0 = __ldg(reinterpret_cast<const uint4*>(src));
+                g1 = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+                u0 = __ldg(reinterpret_cast<const uint4*>(src + I));
+                u1 = __ldg(reinterpret_cast<const uint4*>(src + I) + 1);
             }
-            group_scale<false>(max8(amax16f(u)), sc, inv);
+            float a[16];
+            const uint32_t gw[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+            const uint32_t uw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 g = widen(gw[j]), u = widen(uw[j]);
+                a[2 * j] = g.x * sigmoidf(g.x) * u.x;
+                a[2 * j + 1] = g.y * sigmoidf(g.y) * u.y;
+            }
+            const float ma = max8(amax16f(a));
+            float inv_a, inv_g = 0.0f, inv_u = 0.0f;
+            if (CKPT) {
+                const float mg = max8(amax16(g0, g1)), mu = max8(amax16(u0, u1));
+                float sc, inv;
+                group_scale<false>(sub == 0 ? ma : sub == 1 ? mg : mu, sc, inv);
+                inv_a = __shfl_sync(kFull, inv, 0, 8);
+                inv_g = __shfl_sync(kFull, inv, 1, 8);
+                inv_u = __shfl_sync(kFull, inv, 2, 8);
+                const float ka = __shfl_sync(kFull, sc, 0, 8), kg = __shfl_sync(kFull, sc, 1, 8),
+                            ku = __shfl_sync(kFull, sc, 2, 8);
+                if (sub == i) {
+                    sa = ka;
+                    sg = kg;
+                    su = ku;
+                }
+            } else {
+                float sc;
+                group_scale<false>(ma, sc, inv_a);
+                if (sub == i) sa = sc;
+            }
             if (live) {
-                reinterpret_cast<uint4*>(hq + m * 2 * I + I + ib * 128)[sub] = quant16f(u, inv);
-                if (sub == 0) hs[(IB + ib) * M + m] = sc;
+                *reinterpret_cast<uint4*>(qa) = quant16f(a, inv_a);
+                if (CKPT) {
+                    const uint2 p = quant8(g0, inv_g), r = quant8(g1, inv_g), v = quant8(u0, inv_u), z = quant8(u1, inv_u);
+                    *reinterpret_cast<uint4*>(qh) = make_uint4(p.x, p.y, r.x, r.y);
+                    *reinterpret_cast<uint4*>(qh + I) = make_uint4(v.x, v.y, z.x, z.y);
+                }
+            }
+        }
+        if (live && sub < n) {
+            s[(size_t)ib * M + m0 + sub] = sa;
+            if (CKPT) {
+                hs[(size_t)ib * M + m0 + sub] = sg;
+                hs[(size_t)(IB + ib) * M + m0 + sub] = su;
             }
         }
     }
