@@ -278,8 +278,12 @@ int fp8q_swiglu_backward_quant(const uint16_t* da, const uint8_t* hq, const floa
         !aligned16(st) || !aligned16(aqt) || !aligned16(ast) || !aligned4(offsets))
         return FP8Q_ERR_ALIGN;
     const int64_t tiles = ((M + 127) / 128 + E) * (I / 128);
-    return launch_kernel(swiglu_backward_kernel, dim3(grid_for(tiles, 2)), dim3(256), group_table_bytes(E), (cudaStream_t)stream, false,
-                         da, hq, hs, offsets, (int)E, M, I, q, s, qt, st, aqt, ast, Kcap);
+    if (tiles > kI32) return FP8Q_ERR_UNSUPPORTED;
+    static std::atomic<bool> ready[kMaxDevices];
+    if (!allow_smem(swiglu_backward_kernel, back_smem(kMoeMaxExperts), ready)) return FP8Q_ERR_CUDA;
+    return launch_kernel(swiglu_backward_kernel, dim3(grid_for(tiles, 1)), dim3(kBackThreads), back_smem(E),
+                         (cudaStream_t)stream, false, da, hq, hs, offsets, (int)E, M, (uint32_t)I, q, s, qt, st, aqt, ast,
+                         Kcap);
 }
 
 }  // extern "C"

@@ -857,87 +857,6 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* 
 }
 
 // ------------------------------------------------------------------------------------------
-// Tiles of 128 rows x 128 columns whose values sit in registers (warp w: rows 16w + i, lane l:
-// columns 4l + j), quantised in both directions as act_dual_tile does for bf16 inputs.
-// ------------------------------------------------------------------------------------------
-struct TileScratch {
-    float red[8][128];
-    float inv_c[128];
-    uint4 qs[128 * 8];   // transposed codes, [column][128 rows]
-};
-
-// 1x128 codes of the tile's first `nvalid` rows: to rows r0 .. of q[M, C] and s[C/128][M].
-__device__ __forceinline__ void tile_rows(const float (&v)[16][4], int nvalid, int64_t r0, int64_t c0, int64_t M,
-                                          int64_t C, uint8_t* __restrict__ q, float* __restrict__ s)
-{
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float rm[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        rm[i] = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
-    // Reduce-scatter: the maximum of row 16w + (lane >> 1) ends on lanes 2r, 2r + 1.
-#pragma unroll
-    for (int h = 8; h >= 1; h >>= 1) {
-        const bool up = lane & (2 * h);
-#pragma unroll
-        for (int i = 0; i < h; ++i) {
-            const float send = up ? rm[i] : rm[i + h], keep = up ? rm[i + h] : rm[i];
-            rm[i] = fmaxf(keep, __shfl_xor_sync(kFull, send, 2 * h));
-        }
-    }
-    rm[0] = fmaxf(rm[0], __shfl_xor_sync(kFull, rm[0], 1));
-    float sc, inv;
-    group_scale<false>(rm[0], sc, inv);
-    const int mine = 16 * w + (lane >> 1);
-    if (!(lane & 1) && mine < nvalid) s[(c0 >> 7) * M + r0 + mine] = sc;
-    uint8_t* out = q + (r0 + 16 * w) * C + c0 + 4 * lane;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float ri = __shfl_sync(kFull, inv, 2 * i);
-        if (16 * w + i < nvalid)
-            *reinterpret_cast<uint32_t*>(out + (int64_t)i * C) = e4m3x4(v[i][0], v[i][1], v[i][2], v[i][3], ri);
-    }
-}
-
-// 128x1 codes of the whole tile (rows past its valid ones hold zeros), transposed: to columns 128 g ..
-// of qt[C, Kcap] and st[g][C].  Ends with a barrier, so the scratch can be used again.
-__device__ __forceinline__ void tile_cols(const float (&v)[16][4], int64_t g, int64_t c0, int64_t C, int64_t Kcap,
-                                          uint8_t* __restrict__ qt, float* __restrict__ st, TileScratch& sm)
-{
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float cm[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) cm[j] = fmaxf(cm[j], fabsf(v[i][j]));
-    *reinterpret_cast<float4*>(&sm.red[w][4 * lane]) = make_float4(cm[0], cm[1], cm[2], cm[3]);
-    __syncthreads();
-    if (threadIdx.x < 128) {
-        float a = sm.red[0][threadIdx.x];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) a = fmaxf(a, sm.red[i][threadIdx.x]);
-        float sc, inv;
-        group_scale<false>(a, sc, inv);
-        st[g * C + c0 + threadIdx.x] = sc;
-        sm.inv_c[threadIdx.x] = inv;
-    }
-    __syncthreads();
-    const float4 ic = *reinterpret_cast<const float4*>(&sm.inv_c[4 * lane]);
-    const float inv[4] = {ic.x, ic.y, ic.z, ic.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t c[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-            c[p] = e4m3x4(v[4 * p][j], v[4 * p + 1][j], v[4 * p + 2][j], v[4 * p + 3][j], inv[j]);
-        sm.qs[qt_unit<2>(4 * lane + j, w)] = make_uint4(c[0], c[1], c[2], c[3]);
-    }
-    __syncthreads();
-    qt_store_rows<2, 4>(sm.qs, 16 * w, qt, c0, Kcap, g * 128, lane);
-    __syncthreads();
-}
-
-// ------------------------------------------------------------------------------------------
 // Dispatch, ragged 128x1 codes.  A CTA takes tiles of one padded group (128 rows) x 128 channels; the
 // gathered rows come into shared memory by asynchronous copies, 256 bytes of a row at a time, while the
 // previous tile is quantised.  Warp w quantises channels 16w .. 16w+15: lane (r, h) = (lane >> 1,
@@ -1339,6 +1258,34 @@ __global__ void __launch_bounds__(256, 4) swiglu_quant_kernel(const uint16_t* __
     }
 }
 
+// ------------------------------------------------------------------------------------------
+// SwiGLU backward from the checkpoint h^ = code * scale, r = sigmoid(g):
+//   dg = da u r (1 + g (1 - r)),   du = da g r,   a = g r u
+// Outputs: dh = [dg, du] in both forms (Dgrad's and Wgrad's operand) and a in the 128x1 form (the
+// second GEMM's Wgrad operand), so a is never kept between the passes.
+// One CTA of 16 warps takes tiles of one padded group (128 rows) x 128 columns of I, whose inputs come
+// into shared memory by asynchronous copies while the tile before is worked on.  Warp w owns columns
+// 8w .. 8w+7, its lane r rows 4r .. 4r+3: the 96 values (three an element) are computed once and stay in
+// registers until both quantisations are done.  Columns lie inside a warp, so their scales need shuffles
+// only and their codes leave as whole lines; rows meet in shared memory.
+// The values fill the register file with one CTA an SM; bound by instruction issue, not far above HBM.
+// ------------------------------------------------------------------------------------------
+constexpr int kBackThreads = 512;
+constexpr int kBackStage = 128 * 256 + 2 * 128 * 128 + 2 * 128 * 4;   // da, the codes of g and u, their scales
+struct BackSmem {   // byte offsets
+    static constexpr int codes = 2 * kBackStage;              // row codes of dg and du: [2][128][128]
+    static constexpr int red = codes + 2 * 128 * 128;         // [2][16 warps][128 rows]
+    static constexpr int inv_row = red + 2 * 16 * 128 * 4;    // [2][128]
+    static constexpr int inv_col = inv_row + 2 * 128 * 4;     // [16 warps][24], 32 apart
+    static constexpr int table = inv_col + 16 * 32 * 4;
+};
+constexpr int back_smem(int E) { return BackSmem::table + group_table_bytes(E); }
+
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live)   // zero unless live
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+
 __device__ __forceinline__ void dec_e4m3x4(uint32_t w, float (&f)[4])
 {
     uint32_t h0, h1;
@@ -1348,60 +1295,187 @@ __device__ __forceinline__ void dec_e4m3x4(uint32_t w, float (&f)[4])
     asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(f[2]), "=f"(f[3]) : "r"(h1));
 }
 
-// SwiGLU backward from the checkpoint h^ = code * scale, r = sigmoid(g):
-//   dg = da u r (1 + g (1 - r)),   du = da g r,   a = g r u
-// Outputs: dh = [dg, du] in both forms (Dgrad's and Wgrad's operand) and a in the 128x1 form (the
-// second GEMM's Wgrad operand), so a is never kept between the passes.  One tile of 128 rows x 128
-// columns of I at a time, in three sweeps (dg, du, a) that each recompute from the tile's inputs.
-__global__ void __launch_bounds__(256, 2) swiglu_backward_kernel(
+// max |.| over the warp's 32 lanes of eight values each: lane l ends with that of value l & 7.
+__device__ __forceinline__ float max_of_eight(float (&m)[8], int lane)
+{
+#pragma unroll
+    for (int h = 4; h >= 1; h >>= 1) {
+        const bool up = lane & h;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float send = up ? m[i] : m[i + h], keep = up ? m[i + h] : m[i];
+            m[i] = fmaxf(keep, __shfl_xor_sync(kFull, send, h));
+        }
+    }
+    m[0] = fmaxf(m[0], __shfl_xor_sync(kFull, m[0], 8));
+    return fmaxf(m[0], __shfl_xor_sync(kFull, m[0], 16));
+}
+
+__global__ void __launch_bounds__(kBackThreads, 1) swiglu_backward_kernel(
     const uint16_t* __restrict__ da, const uint8_t* __restrict__ hq, const float* __restrict__ hs,
-    const int32_t* __restrict__ offsets, int E, int64_t M, int64_t I, uint8_t* __restrict__ q, float* __restrict__ s,
+    const int32_t* __restrict__ offsets, int E, int64_t M, uint32_t I, uint8_t* __restrict__ q, float* __restrict__ s,
     uint8_t* __restrict__ qt, float* __restrict__ st, uint8_t* __restrict__ aqt, float* __restrict__ ast, int64_t Kcap)
 {
     griddep_launch_dependents();
     griddep_wait();
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) TileScratch sm;
-    const GroupTable table(smem, E);
+    const GroupTable table(smem + BackSmem::table, E);
     if (!group_table(table, offsets, E, M, Kcap)) return;
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t IB = I >> 7, groups = table.pre[E], tiles = groups * IB;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int g = (int)(tile / IB);
-        const int64_t ib = tile - (int64_t)g * IB;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t IB = I >> 7, groups = table.pre[E], tiles = groups * IB;
+    float* red = reinterpret_cast<float*>(smem + BackSmem::red);
+    float* inv_row = reinterpret_cast<float*>(smem + BackSmem::inv_row);
+    float* inv_col = reinterpret_cast<float*>(smem + BackSmem::inv_col) + 32 * w;
+
+    // Copies of a tile's inputs.  16-byte piece c of a row's 256 (da) or 128 bytes (codes) lies at piece
+    // c ^ ((row >> 2) & 7): eight neighbouring lanes then read different banks.
+    auto fetch = [&](uint32_t tile, int buf) {
+        if (tile < tiles) {
+            const uint32_t g = tile / IB, ib = tile - g * IB;
+            int64_t r0;
+            int nvalid;
+            group_rows(table, E, (int)g, r0, nvalid);
+            const uint32_t dst = base + buf * kBackStage;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (tid >> 4) + 32 * i, c = tid & 15;
+                const int64_t at = r0 + min(row, nvalid - 1);
+                copy16(dst + row * 256 + ((c ^ ((row >> 2) & 7)) << 4), da + at * I + ib * 128 + 8 * c, row < nvalid);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (tid >> 3) + 64 * (i & 1), c = tid & 7;
+                const int64_t at = r0 + min(row, nvalid - 1);
+                copy16(dst + 32768 + 16384 * (i >> 1) + row * 128 + ((c ^ ((row >> 2) & 7)) << 4),
+                       hq + at * 2 * I + (i >> 1) * I + ib * 128 + 16 * c, row < nvalid);
+            }
+            if (tid < 256) {
+                const int row = tid & 127;
+                copy4(dst + 65536 + 4 * tid, hs + (int64_t)((tid >> 7) * IB + ib) * M + r0 + min(row, nvalid - 1),
+                      row < nvalid);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    fetch(blockIdx.x, 0);
+    int buf = 0;
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+        const uint32_t g = tile / IB, ib = tile - g * IB;
         int64_t r0;
         int nvalid;
-        group_rows(table, E, g, r0, nvalid);
-        for (int sweep = 0; sweep < 3; ++sweep) {
-            float v[16][4];
+        group_rows(table, E, (int)g, r0, nvalid);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();   // this tile has landed; the tile before is done with the other buffer
+        fetch(tile + gridDim.x, buf ^ 1);
+
+        const uint8_t* in = smem + buf * kBackStage;
+        float dg[4][8], du[4][8], ac[4][8];
+        float4 rg, ru;   // row maxima of dg and du
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int n = 16 * w + i;
-                v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.0f;
-                if (n < nvalid) {
-                    const int64_t r = r0 + n;
-                    const uint2 d = __ldg(reinterpret_cast<const uint2*>(da + r * I + ib * 128) + lane);
-                    const uint32_t gc = __ldg(reinterpret_cast<const uint32_t*>(hq + r * 2 * I + ib * 128) + lane);
-                    const uint32_t uc = __ldg(reinterpret_cast<const uint32_t*>(hq + r * 2 * I + I + ib * 128) + lane);
-                    const float gs = __ldg(hs + ib * M + r), us = __ldg(hs + (IB + ib) * M + r);
-                    float gf[4], uf[4];
-                    dec_e4m3x4(gc, gf);
-                    dec_e4m3x4(uc, uf);
-                    const float df[4] = {bf16_lo(d.x), bf16_hi(d.x), bf16_lo(d.y), bf16_hi(d.y)};
+        for (int i = 0; i < 4; ++i) {
+            const int row = 4 * lane + i;
+            const uint4 dw = *reinterpret_cast<const uint4*>(in + row * 256 + ((w ^ (lane & 7)) << 4));
+            const uint2 gc = *reinterpret_cast<const uint2*>(in + 32768 + row * 128 + (((w >> 1) ^ (lane & 7)) << 4) + 8 * (w & 1));
+            const uint2 uc = *reinterpret_cast<const uint2*>(in + 49152 + row * 128 + (((w >> 1) ^ (lane & 7)) << 4) + 8 * (w & 1));
+            const float gs = *reinterpret_cast<const float*>(in + 65536 + 4 * row);
+            const float us = *reinterpret_cast<const float*>(in + 65536 + 512 + 4 * row);
+            float mg = 0.0f, mu = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x = gf[j] * gs, u = uf[j] * us, rr = sigmoidf(x), a = x * rr;
-                        v[i][j] = sweep == 0 ? df[j] * u * (rr + a * (1.0f - rr)) : sweep == 1 ? df[j] * a : a * u;
-                    }
+            for (int p = 0; p < 2; ++p) {
+                float gf[4], uf[4];
+                dec_e4m3x4(p ? gc.y : gc.x, gf);
+                dec_e4m3x4(p ? uc.y : uc.x, uf);
+                const float2 d0 = widen(p ? dw.z : dw.x), d1 = widen(p ? dw.w : dw.y);
+                const float d[4] = {d0.x, d0.y, d1.x, d1.y};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x = gf[j] * gs, u = uf[j] * us, r = sigmoidf(x), sx = x * r;
+                    const int c = 4 * p + j;
+                    dg[i][c] = d[j] * u * fmaf(sx, 1.0f - r, r);
+                    du[i][c] = d[j] * sx;
+                    ac[i][c] = u * sx;
+                    mg = fmaxf(mg, fabsf(dg[i][c]));
+                    mu = fmaxf(mu, fabsf(du[i][c]));
                 }
             }
-            const int64_t c0 = (sweep == 1 ? I : 0) + ib * 128;
-            if (sweep < 2) {
-                tile_rows(v, nvalid, r0, c0, M, 2 * I, q, s);
-                tile_cols(v, g, c0, 2 * I, Kcap, qt, st, sm);
-            } else {
-                tile_cols(v, g, c0, I, Kcap, aqt, ast, sm);
+            (i == 0 ? rg.x : i == 1 ? rg.y : i == 2 ? rg.z : rg.w) = mg;
+            (i == 0 ? ru.x : i == 1 ? ru.y : i == 2 ? ru.z : ru.w) = mu;
+        }
+        *reinterpret_cast<float4*>(red + w * 128 + 4 * lane) = rg;
+        *reinterpret_cast<float4*>(red + 2048 + w * 128 + 4 * lane) = ru;
+        __syncthreads();
+        if (tid < 256) {   // the row scales: thread (dg or du, row)
+            const int row = tid & 127;
+            const float* p = red + (tid >> 7) * 2048 + row;
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = fmaxf(m, p[128 * i]);
+            float sc, inv;
+            group_scale<false>(m, sc, inv);
+            inv_row[tid] = inv;
+            if (row < nvalid) s[(int64_t)((tid >> 7) * IB + ib) * M + r0 + row] = sc;
+        }
+        // Columns.  Lanes 8v + c: the scale of column c of value v (dg, du, a).
+        {
+            float m[8], mine;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                m[c] = fmaxf(fmaxf(fabsf(dg[0][c]), fabsf(dg[1][c])), fmaxf(fabsf(dg[2][c]), fabsf(dg[3][c])));
+            mine = max_of_eight(m, lane);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                m[c] = fmaxf(fmaxf(fabsf(du[0][c]), fabsf(du[1][c])), fmaxf(fabsf(du[2][c]), fabsf(du[3][c])));
+            const float m1 = max_of_eight(m, lane);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                m[c] = fmaxf(fmaxf(fabsf(ac[0][c]), fabsf(ac[1][c])), fmaxf(fabsf(ac[2][c]), fabsf(ac[3][c])));
+            const float m2 = max_of_eight(m, lane);
+            const int v = lane >> 3;
+            mine = v == 0 ? mine : v == 1 ? m1 : m2;
+            float sc, inv;
+            group_scale<false>(mine, sc, inv);
+            const uint32_t col = ib * 128 + 8 * w + (lane & 7);
+            if (v < 2) st[(int64_t)g * 2 * I + v * I + col] = sc;
+            if (v == 2) ast[(int64_t)g * I + col] = sc;
+            if (v < 3) inv_col[lane] = inv;
+        }
+        __syncwarp();
+        const int64_t col0 = ib * 128 + 8 * w;
+        auto columns = [&](const float (&x)[4][8], const float* inv, uint8_t* out) {
+            out += col0 * Kcap + (int64_t)g * 128 + 4 * lane;
+            const float4 i0 = *reinterpret_cast<const float4*>(inv), i1 = *reinterpret_cast<const float4*>(inv + 4);
+            const float f[8] = {i0.x, i0.y, i0.z, i0.w, i1.x, i1.y, i1.z, i1.w};
+#pragma unroll
+            for (int c = 0; c < 8; ++c, out += Kcap)
+                *reinterpret_cast<uint32_t*>(out) = e4m3x4(x[0][c], x[1][c], x[2][c], x[3][c], f[c]);
+        };
+        columns(ac, inv_col + 16, aqt);
+        columns(dg, inv_col, qt);
+        columns(du, inv_col + 8, qt + (int64_t)I * Kcap);
+        __syncthreads();
+        // Rows: 8 bytes of a row from each warp, staged (8-byte unit w of row r at w ^ ((r >> 2) & 15)) and
+        // written as whole lines.
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const float4 i4 = *reinterpret_cast<const float4*>(inv_row + 128 * v + 4 * lane);
+            const float f[4] = {i4.x, i4.y, i4.z, i4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float (&x)[8] = v ? du[i] : dg[i];
+                *reinterpret_cast<uint2*>(smem + BackSmem::codes + v * 16384 + (4 * lane + i) * 128 + ((w ^ (lane & 15)) << 3)) =
+                    make_uint2(e4m3x4(x[0], x[1], x[2], x[3], f[i]), e4m3x4(x[4], x[5], x[6], x[7], f[i]));
             }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int v = i >> 1, row = (tid >> 3) + 64 * (i & 1), c = tid & 7, f = (row >> 2) & 15;
+            const uint4 u = *reinterpret_cast<const uint4*>(smem + BackSmem::codes + v * 16384 + row * 128 + (((2 * c) ^ (f & 14)) << 3));
+            if (row < nvalid)
+                *reinterpret_cast<uint4*>(q + (r0 + row) * 2 * I + v * I + ib * 128 + 16 * c) =
+                    (f & 1) ? make_uint4(u.z, u.w, u.x, u.y) : u;
         }
     }
 }
