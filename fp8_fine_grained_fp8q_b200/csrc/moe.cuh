@@ -769,6 +769,32 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, d;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 c, a, b;\n\t"
+        "mov.b64 {%0, %1}, c;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 widen(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 __device__ __forceinline__ uint32_t abs2(uint32_t w) { return w & 0x7FFF7FFFu; }
 // Larger of each of two bf16 pairs; a NaN loses, as in fmaxf.
@@ -1178,9 +1204,19 @@ __global__ void __launch_bounds__(256) moe_combine_dweight_kernel(const uint16_t
 // 32-byte sectors.  One lane of the eight forms each of the three scales.
 // Bound by HBM; the two MUFU operations an element take 60 us of 65536 x 2048, the bytes 145.
 // ------------------------------------------------------------------------------------------
-// sigmoid by ex2 and a fast reciprocal: relative error below (4 + 1.2 |x|) 2^-23; x = -inf gives 0, and
-// beyond |x| = 88 the result is 0 or 1 as binary32 has it.
-__device__ __forceinline__ float sigmoidf(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// sigmoid of two values by ex2 and a fast reciprocal: with the rounding of x log2 e, a relative error below
+// (4 + 1.5 |x|) 2^-24 and a few steps of the two functions; beyond |x| = 88 the result is 0 or 1.
+__device__ __forceinline__ float2 sigmoid2(float2 x)
+{
+    const float2 t = mul2(x, both(-1.442695041f));   // -log2 e
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = add2(e, both(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    return e;
+}
 
 template <bool CKPT>
 __global__ void __launch_bounds__(256, 4) swiglu_quant_kernel(const uint16_t* __restrict__ h, uint32_t M, uint32_t I,
@@ -1214,9 +1250,9 @@ __global__ void __launch_bounds__(256, 4) swiglu_quant_kernel(const uint16_t* __
             const uint32_t uw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float2 g = widen(gw[j]), u = widen(uw[j]);
-                a[2 * j] = g.x * sigmoidf(g.x) * u.x;
-                a[2 * j + 1] = g.y * sigmoidf(g.y) * u.y;
+                const float2 g = widen(gw[j]), v = mul2(mul2(g, sigmoid2(g)), widen(uw[j]));
+                a[2 * j] = v.x;
+                a[2 * j + 1] = v.y;
             }
             const float ma = max8(amax16f(a));
             float inv_a, inv_g = 0.0f, inv_u = 0.0f;
@@ -1277,7 +1313,8 @@ struct BackSmem {   // byte offsets
     static constexpr int red = codes + 2 * 128 * 128;         // [2][16 warps][128 rows]
     static constexpr int inv_row = red + 2 * 16 * 128 * 4;    // [2][128]
     static constexpr int inv_col = inv_row + 2 * 128 * 4;     // [16 warps][24], 32 apart
-    static constexpr int table = inv_col + 16 * 32 * 4;
+    static constexpr int place = inv_col + 16 * 32 * 4;       // [3] int4
+    static constexpr int table = place + 64;
 };
 constexpr int back_smem(int E) { return BackSmem::table + group_table_bytes(E); }
 
@@ -1286,13 +1323,22 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
 
-__device__ __forceinline__ void dec_e4m3x4(uint32_t w, float (&f)[4])
+// The values of four E4M3 codes.
+__device__ __forceinline__ void dec_e4m3x4(uint32_t w, float2 (&f)[2])
 {
-    uint32_t h0, h1;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"((uint16_t)(w & 0xFFFFu)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"((uint16_t)(w >> 16)));
-    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(f[0]), "=f"(f[1]) : "r"(h0));
-    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(f[2]), "=f"(f[3]) : "r"(h1));
+    asm("{.reg .b16 c0, c1, l, h;\n\t"
+        ".reg .b32 p;\n\t"
+        "mov.b32 {c0, c1}, %4;\n\t"
+        "cvt.rn.f16x2.e4m3x2 p, c0;\n\t"
+        "mov.b32 {l, h}, p;\n\t"
+        "cvt.f32.f16 %0, l;\n\t"
+        "cvt.f32.f16 %1, h;\n\t"
+        "cvt.rn.f16x2.e4m3x2 p, c1;\n\t"
+        "mov.b32 {l, h}, p;\n\t"
+        "cvt.f32.f16 %2, l;\n\t"
+        "cvt.f32.f16 %3, h;}"
+        : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y)
+        : "r"(w));
 }
 
 // max |.| over the warp's 32 lanes of eight values each: lane l ends with that of value l & 7.
@@ -1328,51 +1374,70 @@ __global__ void __launch_bounds__(kBackThreads, 1) swiglu_backward_kernel(
     float* inv_row = reinterpret_cast<float*>(smem + BackSmem::inv_row);
     float* inv_col = reinterpret_cast<float*>(smem + BackSmem::inv_col) + 32 * w;
 
-    // Copies of a tile's inputs.  16-byte piece c of a row's 256 (da) or 128 bytes (codes) lies at piece
-    // c ^ ((row >> 2) & 7): eight neighbouring lanes then read different banks.
-    auto fetch = [&](uint32_t tile, int buf) {
-        if (tile < tiles) {
-            const uint32_t g = tile / IB, ib = tile - g * IB;
+    // A tile's place, looked up by one warp two tiles ahead: first row, rows, group, column block.
+    int4* place = reinterpret_cast<int4*>(smem + BackSmem::place);
+    auto look_up = [&](uint32_t tile, int slot) {
+        if (w == kBackThreads / 32 - 1 && tile < tiles) {
+            const uint32_t ib = tile / groups, g = tile - ib * groups;
             int64_t r0;
             int nvalid;
             group_rows(table, E, (int)g, r0, nvalid);
+            if (lane == 0) place[slot] = make_int4((int)r0, nvalid, (int)g, (int)ib);
+        }
+    };
+    // Copies of a tile's inputs.  16-byte piece c of a row's 256 (da) or 128 bytes (codes) lies at piece
+    // c ^ ((row >> 2) & 7): eight neighbouring lanes then read different banks.
+    auto fetch = [&](uint32_t tile, int slot, int buf) {
+        if (tile < tiles) {
+            const int4 at = place[slot];
             const uint32_t dst = base + buf * kBackStage;
+            {
+                const int row = tid >> 4, c = tid & 15;
+                const uint16_t* src = da + (int64_t)at.x * I + at.w * 128 + 8 * c;
+                const uint32_t to = dst + row * 256 + ((c ^ ((row >> 2) & 7)) << 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = (tid >> 4) + 32 * i, c = tid & 15;
-                const int64_t at = r0 + min(row, nvalid - 1);
-                copy16(dst + row * 256 + ((c ^ ((row >> 2) & 7)) << 4), da + at * I + ib * 128 + 8 * c, row < nvalid);
+                for (int i = 0; i < 4; ++i) {   // rows 32 apart: the same swizzle
+                    const bool live = row + 32 * i < at.y;
+                    copy16(to + i * 32 * 256, src + (uint64_t)(live ? (uint32_t)(row + 32 * i) : 0u) * I, live);
+                }
             }
+            {
+                const int row = tid >> 3, c = tid & 7;
+                const uint8_t* src = hq + (int64_t)at.x * 2 * I + at.w * 128 + 16 * c;
+                const uint32_t to = dst + 32768 + row * 128 + ((c ^ ((row >> 2) & 7)) << 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = (tid >> 3) + 64 * (i & 1), c = tid & 7;
-                const int64_t at = r0 + min(row, nvalid - 1);
-                copy16(dst + 32768 + 16384 * (i >> 1) + row * 128 + ((c ^ ((row >> 2) & 7)) << 4),
-                       hq + at * 2 * I + (i >> 1) * I + ib * 128 + 16 * c, row < nvalid);
+                for (int i = 0; i < 4; ++i) {
+                    const bool live = row + 64 * (i & 1) < at.y;
+                    copy16(to + 16384 * (i >> 1) + 64 * 128 * (i & 1),
+                           src + (uint64_t)(live ? (uint32_t)(row + 64 * (i & 1)) : 0u) * (2 * I) + (i >> 1) * I, live);
+                }
             }
             if (tid < 256) {
                 const int row = tid & 127;
-                copy4(dst + 65536 + 4 * tid, hs + (int64_t)((tid >> 7) * IB + ib) * M + r0 + min(row, nvalid - 1),
-                      row < nvalid);
+                const bool live = row < at.y;
+                copy4(dst + 65536 + 4 * tid, hs + (int64_t)((tid >> 7) * IB + at.w) * M + at.x + (live ? row : 0), live);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    fetch(blockIdx.x, 0);
-    int buf = 0;
-    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
-        const uint32_t g = tile / IB, ib = tile - g * IB;
-        int64_t r0;
-        int nvalid;
-        group_rows(table, E, (int)g, r0, nvalid);
+    look_up(blockIdx.x, 0);
+    look_up(blockIdx.x + gridDim.x, 1);
+    __syncthreads();
+    fetch(blockIdx.x, 0, 0);
+    int buf = 0, slot = 0;
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1, slot = slot == 2 ? 0 : slot + 1) {
+        const int4 at = place[slot];
+        const int64_t r0 = at.x;
+        const int nvalid = at.y, g = at.z, ib = at.w;
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();   // this tile has landed; the tile before is done with the other buffer
-        fetch(tile + gridDim.x, buf ^ 1);
+        fetch(tile + gridDim.x, slot == 2 ? 0 : slot + 1, buf ^ 1);
+        look_up(tile + 2 * gridDim.x, slot == 0 ? 2 : slot - 1);
 
         const uint8_t* in = smem + buf * kBackStage;
-        float dg[4][8], du[4][8], ac[4][8];
-        float4 rg, ru;   // row maxima of dg and du
+        float2 dg[4][4], du[4][4], ac[4][4];   // [row][pair of columns]
+        float rg[4], ru[4];                    // row maxima of dg and du
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 4 * lane + i;
@@ -1381,93 +1446,89 @@ __global__ void __launch_bounds__(kBackThreads, 1) swiglu_backward_kernel(
             const uint2 uc = *reinterpret_cast<const uint2*>(in + 49152 + row * 128 + (((w >> 1) ^ (lane & 7)) << 4) + 8 * (w & 1));
             const float gs = *reinterpret_cast<const float*>(in + 65536 + 4 * row);
             const float us = *reinterpret_cast<const float*>(in + 65536 + 512 + 4 * row);
-            float mg = 0.0f, mu = 0.0f;
+            rg[i] = ru[i] = 0.0f;
+            float2 gf[4], uf[4];
+            dec_e4m3x4(gc.x, reinterpret_cast<float2 (&)[2]>(gf[0]));
+            dec_e4m3x4(gc.y, reinterpret_cast<float2 (&)[2]>(gf[2]));
+            dec_e4m3x4(uc.x, reinterpret_cast<float2 (&)[2]>(uf[0]));
+            dec_e4m3x4(uc.y, reinterpret_cast<float2 (&)[2]>(uf[2]));
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                float gf[4], uf[4];
-                dec_e4m3x4(p ? gc.y : gc.x, gf);
-                dec_e4m3x4(p ? uc.y : uc.x, uf);
-                const float2 d0 = widen(p ? dw.z : dw.x), d1 = widen(p ? dw.w : dw.y);
-                const float d[4] = {d0.x, d0.y, d1.x, d1.y};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float x = gf[j] * gs, u = uf[j] * us, r = sigmoidf(x), sx = x * r;
-                    const int c = 4 * p + j;
-                    dg[i][c] = d[j] * u * fmaf(sx, 1.0f - r, r);
-                    du[i][c] = d[j] * sx;
-                    ac[i][c] = u * sx;
-                    mg = fmaxf(mg, fabsf(dg[i][c]));
-                    mu = fmaxf(mu, fabsf(du[i][c]));
-                }
+            for (int j = 0; j < 4; ++j) {
+                const float2 d = widen(word(dw, j)), x = mul2(gf[j], both(gs)), u = mul2(uf[j], both(us));
+                const float2 r = sigmoid2(x), sx = mul2(x, r);
+                // r + sx (1 - r)
+                dg[i][j] = mul2(mul2(d, u), fma2(sx, fma2(r, both(-1.0f), both(1.0f)), r));
+                du[i][j] = mul2(d, sx);
+                ac[i][j] = mul2(u, sx);
+                rg[i] = fmaxf(fmaxf(rg[i], fabsf(dg[i][j].x)), fabsf(dg[i][j].y));
+                ru[i] = fmaxf(fmaxf(ru[i], fabsf(du[i][j].x)), fabsf(du[i][j].y));
             }
-            (i == 0 ? rg.x : i == 1 ? rg.y : i == 2 ? rg.z : rg.w) = mg;
-            (i == 0 ? ru.x : i == 1 ? ru.y : i == 2 ? ru.z : ru.w) = mu;
         }
-        *reinterpret_cast<float4*>(red + w * 128 + 4 * lane) = rg;
-        *reinterpret_cast<float4*>(red + 2048 + w * 128 + 4 * lane) = ru;
+        *reinterpret_cast<float4*>(red + w * 128 + 4 * lane) = make_float4(rg[0], rg[1], rg[2], rg[3]);
+        *reinterpret_cast<float4*>(red + 2048 + w * 128 + 4 * lane) = make_float4(ru[0], ru[1], ru[2], ru[3]);
         __syncthreads();
         if (tid < 256) {   // the row scales: thread (dg or du, row)
             const int row = tid & 127;
             const float* p = red + (tid >> 7) * 2048 + row;
             float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) m = fmaxf(m, p[128 * i]);
+            for (int i = 0; i < 16; i += 2) m = fmaxf(fmaxf(m, p[128 * i]), p[128 * i + 128]);
             float sc, inv;
             group_scale<false>(m, sc, inv);
             inv_row[tid] = inv;
             if (row < nvalid) s[(int64_t)((tid >> 7) * IB + ib) * M + r0 + row] = sc;
         }
         // Columns.  Lanes 8v + c: the scale of column c of value v (dg, du, a).
+        auto column_max = [&](const float2 (&x)[4][4]) {
+            float m[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                m[2 * j] = fmaxf(fmaxf(fmaxf(fabsf(x[0][j].x), fabsf(x[1][j].x)), fabsf(x[2][j].x)), fabsf(x[3][j].x));
+                m[2 * j + 1] = fmaxf(fmaxf(fmaxf(fabsf(x[0][j].y), fabsf(x[1][j].y)), fabsf(x[2][j].y)), fabsf(x[3][j].y));
+            }
+            return max_of_eight(m, lane);
+        };
         {
-            float m[8], mine;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                m[c] = fmaxf(fmaxf(fabsf(dg[0][c]), fabsf(dg[1][c])), fmaxf(fabsf(dg[2][c]), fabsf(dg[3][c])));
-            mine = max_of_eight(m, lane);
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                m[c] = fmaxf(fmaxf(fabsf(du[0][c]), fabsf(du[1][c])), fmaxf(fabsf(du[2][c]), fabsf(du[3][c])));
-            const float m1 = max_of_eight(m, lane);
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                m[c] = fmaxf(fmaxf(fabsf(ac[0][c]), fabsf(ac[1][c])), fmaxf(fabsf(ac[2][c]), fabsf(ac[3][c])));
-            const float m2 = max_of_eight(m, lane);
+            const float m0 = column_max(dg), m1 = column_max(du), m2 = column_max(ac);
             const int v = lane >> 3;
-            mine = v == 0 ? mine : v == 1 ? m1 : m2;
             float sc, inv;
-            group_scale<false>(mine, sc, inv);
+            group_scale<false>(v == 0 ? m0 : v == 1 ? m1 : m2, sc, inv);
             const uint32_t col = ib * 128 + 8 * w + (lane & 7);
             if (v < 2) st[(int64_t)g * 2 * I + v * I + col] = sc;
             if (v == 2) ast[(int64_t)g * I + col] = sc;
             if (v < 3) inv_col[lane] = inv;
         }
         __syncwarp();
-        const int64_t col0 = ib * 128 + 8 * w;
-        auto columns = [&](const float (&x)[4][8], const float* inv, uint8_t* out) {
-            out += col0 * Kcap + (int64_t)g * 128 + 4 * lane;
+        const int64_t corner = (int64_t)(ib * 128 + 8 * w) * Kcap + (int64_t)g * 128 + 4 * lane;
+        auto columns = [&](const float2 (&x)[4][4], const float* inv, uint8_t* out) {
             const float4 i0 = *reinterpret_cast<const float4*>(inv), i1 = *reinterpret_cast<const float4*>(inv + 4);
-            const float f[8] = {i0.x, i0.y, i0.z, i0.w, i1.x, i1.y, i1.z, i1.w};
+            const float2 f[4] = {{i0.x, i0.y}, {i0.z, i0.w}, {i1.x, i1.y}, {i1.z, i1.w}};
 #pragma unroll
-            for (int c = 0; c < 8; ++c, out += Kcap)
-                *reinterpret_cast<uint32_t*>(out) = e4m3x4(x[0][c], x[1][c], x[2][c], x[3][c], f[c]);
+            for (int j = 0; j < 4; ++j) {
+                const float2 a = mul2(x[0][j], f[j]), b = mul2(x[1][j], f[j]), c = mul2(x[2][j], f[j]), d = mul2(x[3][j], f[j]);
+                *reinterpret_cast<uint32_t*>(out + (uint64_t)(2 * j) * (uint32_t)Kcap) = codes4(a.x, b.x, c.x, d.x);
+                *reinterpret_cast<uint32_t*>(out + (uint64_t)(2 * j + 1) * (uint32_t)Kcap) = codes4(a.y, b.y, c.y, d.y);
+            }
         };
-        columns(ac, inv_col + 16, aqt);
-        columns(dg, inv_col, qt);
-        columns(du, inv_col + 8, qt + (int64_t)I * Kcap);
+        columns(ac, inv_col + 16, aqt + corner);
+        columns(dg, inv_col, qt + corner);
+        columns(du, inv_col + 8, qt + (int64_t)I * Kcap + corner);
         __syncthreads();
         // Rows: 8 bytes of a row from each warp, staged (8-byte unit w of row r at w ^ ((r >> 2) & 15)) and
         // written as whole lines.
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const float4 i4 = *reinterpret_cast<const float4*>(inv_row + 128 * v + 4 * lane);
+        auto stage_rows = [&](const float2 (&x)[4][4], const float* inv, uint8_t* to) {
+            const float4 i4 = *reinterpret_cast<const float4*>(inv + 4 * lane);
             const float f[4] = {i4.x, i4.y, i4.z, i4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float (&x)[8] = v ? du[i] : dg[i];
-                *reinterpret_cast<uint2*>(smem + BackSmem::codes + v * 16384 + (4 * lane + i) * 128 + ((w ^ (lane & 15)) << 3)) =
-                    make_uint2(e4m3x4(x[0], x[1], x[2], x[3], f[i]), e4m3x4(x[4], x[5], x[6], x[7], f[i]));
+                const float2 a = mul2(x[i][0], both(f[i])), b = mul2(x[i][1], both(f[i])), c = mul2(x[i][2], both(f[i])),
+                             d = mul2(x[i][3], both(f[i]));
+                *reinterpret_cast<uint2*>(to + (4 * lane + i) * 128 + ((w ^ (lane & 15)) << 3)) =
+                    make_uint2(codes4(a.x, a.y, b.x, b.y), codes4(c.x, c.y, d.x, d.y));
             }
-        }
+        };
+        stage_rows(dg, inv_row, smem + BackSmem::codes);
+        stage_rows(du, inv_row + 128, smem + BackSmem::codes + 16384);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
