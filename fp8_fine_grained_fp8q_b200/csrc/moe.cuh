@@ -720,11 +720,23 @@ __device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (
         f[2 * i + 1] = bf16_hi(u[i]);
     }
 }
+// max(m, |a|, |b|), a NaN losing (max.f32 with three inputs).
+__device__ __forceinline__ float max_abs(float m, float a, float b)
+{
+    float r;
+    asm("{.reg .f32 a, b;\n\t"
+        "abs.f32 a, %2;\n\t"
+        "abs.f32 b, %3;\n\t"
+        "max.f32 %0, %1, a, b;}"
+        : "=f"(r)
+        : "f"(m), "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float amax16f(const float (&f)[16])
 {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
+    for (int i = 0; i < 16; i += 2) m = max_abs(m, f[i], f[i + 1]);
     return m;
 }
 // Four codes of four values, the first in the low byte.
@@ -1313,7 +1325,7 @@ struct BackSmem {   // byte offsets
     static constexpr int red = codes + 2 * 128 * 128;         // [2][16 warps][128 rows]
     static constexpr int inv_row = red + 2 * 16 * 128 * 4;    // [2][128]
     static constexpr int inv_col = inv_row + 2 * 128 * 4;     // [16 warps][24], 32 apart
-    static constexpr int place = inv_col + 16 * 32 * 4;       // [3] int4
+    static constexpr int place = inv_col + 16 * 32 * 4;       // [4] int4
     static constexpr int table = place + 64;
 };
 constexpr int back_smem(int E) { return BackSmem::table + group_table_bytes(E); }
@@ -1421,19 +1433,32 @@ __global__ void __launch_bounds__(kBackThreads, 1) swiglu_backward_kernel(
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
+    // The staged row codes of a tile (below) as whole lines.
+    auto store_rows = [&](const int4& at) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int v = i >> 1, row = (tid >> 3) + 64 * (i & 1), c = tid & 7, f = (row >> 2) & 15;
+            const uint4 u = *reinterpret_cast<const uint4*>(smem + BackSmem::codes + v * 16384 + row * 128 + (((2 * c) ^ (f & 14)) << 3));
+            if (row < at.y)
+                *reinterpret_cast<uint4*>(q + (int64_t)(at.x + row) * 2 * I + v * I + at.w * 128 + 16 * c) =
+                    (f & 1) ? make_uint4(u.z, u.w, u.x, u.y) : u;
+        }
+    };
+
     look_up(blockIdx.x, 0);
     look_up(blockIdx.x + gridDim.x, 1);
     __syncthreads();
     fetch(blockIdx.x, 0, 0);
-    int buf = 0, slot = 0;
-    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1, slot = slot == 2 ? 0 : slot + 1) {
+    int buf = 0, slot = 0;   // slot: the tile's number modulo 4
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1, slot = (slot + 1) & 3) {
         const int4 at = place[slot];
         const int64_t r0 = at.x;
         const int nvalid = at.y, g = at.z, ib = at.w;
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();   // this tile has landed; the tile before is done with the other buffer
-        fetch(tile + gridDim.x, slot == 2 ? 0 : slot + 1, buf ^ 1);
-        look_up(tile + 2 * gridDim.x, slot == 0 ? 2 : slot - 1);
+        fetch(tile + gridDim.x, (slot + 1) & 3, buf ^ 1);
+        look_up(tile + 2 * gridDim.x, (slot + 2) & 3);
+        if (tile != blockIdx.x) store_rows(place[(slot + 3) & 3]);   // the tile before's
 
         const uint8_t* in = smem + buf * kBackStage;
         float2 dg[4][4], du[4][4], ac[4][4];   // [row][pair of columns]
@@ -1460,8 +1485,8 @@ __global__ void __launch_bounds__(kBackThreads, 1) swiglu_backward_kernel(
                 dg[i][j] = mul2(mul2(d, u), fma2(sx, fma2(r, both(-1.0f), both(1.0f)), r));
                 du[i][j] = mul2(d, sx);
                 ac[i][j] = mul2(u, sx);
-                rg[i] = fmaxf(fmaxf(rg[i], fabsf(dg[i][j].x)), fabsf(dg[i][j].y));
-                ru[i] = fmaxf(fmaxf(ru[i], fabsf(du[i][j].x)), fabsf(du[i][j].y));
+                rg[i] = max_abs(rg[i], dg[i][j].x, dg[i][j].y);
+                ru[i] = max_abs(ru[i], du[i][j].x, du[i][j].y);
             }
         }
         *reinterpret_cast<float4*>(red + w * 128 + 4 * lane) = make_float4(rg[0], rg[1], rg[2], rg[3]);
@@ -1483,8 +1508,8 @@ __global__ void __launch_bounds__(kBackThreads, 1) swiglu_backward_kernel(
             float m[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                m[2 * j] = fmaxf(fmaxf(fmaxf(fabsf(x[0][j].x), fabsf(x[1][j].x)), fabsf(x[2][j].x)), fabsf(x[3][j].x));
-                m[2 * j + 1] = fmaxf(fmaxf(fmaxf(fabsf(x[0][j].y), fabsf(x[1][j].y)), fabsf(x[2][j].y)), fabsf(x[3][j].y));
+                m[2 * j] = max_abs(max_abs(0.0f, x[0][j].x, x[1][j].x), x[2][j].x, x[3][j].x);
+                m[2 * j + 1] = max_abs(max_abs(0.0f, x[0][j].y, x[1][j].y), x[2][j].y, x[3][j].y);
             }
             return max_of_eight(m, lane);
         };
@@ -1514,8 +1539,8 @@ __global__ void __launch_bounds__(kBackThreads, 1) swiglu_backward_kernel(
         columns(dg, inv_col, qt + corner);
         columns(du, inv_col + 8, qt + (int64_t)I * Kcap + corner);
         __syncthreads();
-        // Rows: 8 bytes of a row from each warp, staged (8-byte unit w of row r at w ^ ((r >> 2) & 15)) and
-        // written as whole lines.
+        // Rows: 8 bytes of a row from each warp, staged (8-byte unit w of row r at w ^ ((r >> 2) & 15)); they
+        // are written behind the next tile's first barrier.
         auto stage_rows = [&](const float2 (&x)[4][4], const float* inv, uint8_t* to) {
             const float4 i4 = *reinterpret_cast<const float4*>(inv + 4 * lane);
             const float f[4] = {i4.x, i4.y, i4.z, i4.w};
@@ -1529,16 +1554,9 @@ __global__ void __launch_bounds__(kBackThreads, 1) swiglu_backward_kernel(
         };
         stage_rows(dg, inv_row, smem + BackSmem::codes);
         stage_rows(du, inv_row + 128, smem + BackSmem::codes + 16384);
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int v = i >> 1, row = (tid >> 3) + 64 * (i & 1), c = tid & 7, f = (row >> 2) & 15;
-            const uint4 u = *reinterpret_cast<const uint4*>(smem + BackSmem::codes + v * 16384 + row * 128 + (((2 * c) ^ (f & 14)) << 3));
-            if (row < nvalid)
-                *reinterpret_cast<uint4*>(q + (r0 + row) * 2 * I + v * I + ib * 128 + 16 * c) =
-                    (f & 1) ? make_uint4(u.z, u.w, u.x, u.y) : u;
-        }
     }
+    __syncthreads();
+    if (blockIdx.x < tiles) store_rows(place[(slot + 3) & 3]);
 }
 
 }  // namespace fp8q
