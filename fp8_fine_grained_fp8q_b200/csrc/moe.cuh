@@ -807,7 +807,19 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return r;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 widen(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+// Two bf16 values as FP32, by a mixed-precision x + (-0), which is x: it runs on the FMA pipe, whereas
+// shifting and masking take the ALU, which the conversions to E4M3 and the maxima already fill.
+__device__ __forceinline__ float2 widen(uint32_t w)
+{
+    float2 r;
+    asm("{.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "add.f32.bf16 %0, l, %3;\n\t"
+        "add.f32.bf16 %1, h, %3;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(w), "f"(-0.0f));
+    return r;
+}
 __device__ __forceinline__ uint32_t abs2(uint32_t w) { return w & 0x7FFF7FFFu; }
 // Larger of each of two bf16 pairs; a NaN loses, as in fmaxf.
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
@@ -835,24 +847,39 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* 
     const uint32_t M = T * k, CB = C >> 7, quads = (CB + 3) >> 2, items = T * quads;
     const int lane = threadIdx.x & 31, sub = lane & 7;
     const uint32_t warps = (gridDim.x * blockDim.x) >> 5;
-    for (uint32_t it = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items; it += warps) {
+    // An item's loads are issued before the item ahead of it is written: behind those writes they take
+    // several microseconds.
+    uint4 a, b;
+    int32_t row;
+    float wt;
+    auto load = [&](uint32_t it, uint4& a, uint4& b, int32_t& row, float& wt) {
         const uint32_t t = it / quads, kb = (it - t * quads) * 4 + (lane >> 3);
-        const bool live = kb < CB;
-        int32_t row = -1;
-        float wt = 1.0f;
-        if (lane < k) {
+        row = -1;
+        wt = 1.0f;
+        if (lane < k && it < items) {
             row = __ldg(rows + t * k + lane);
             if (WEIGHTED) wt = __ldg(weights + t * k + lane);
-            if (row < 0 || row >= (int32_t)M) {
-                latch_status(kDevBadIndex);
-                row = -1;
-            }
         }
-        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-        if (live) {
+        a = make_uint4(0u, 0u, 0u, 0u);
+        b = a;
+        if (kb < CB && it < items) {
             const uint4* p = reinterpret_cast<const uint4*>(x + (size_t)t * C + kb * 128) + 2 * sub;
             a = __ldg(p);
             b = __ldg(p + 1);
+        }
+    };
+    uint32_t it = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    if (it < items) load(it, a, b, row, wt);
+    uint4 next_a, next_b;
+    int32_t next_row;
+    float next_wt;
+    for (; it < items; it += warps, a = next_a, b = next_b, row = next_row, wt = next_wt) {
+        load(it + warps, next_a, next_b, next_row, next_wt);
+        const uint32_t t = it / quads, kb = (it - t * quads) * 4 + (lane >> 3);
+        const bool live = kb < CB;
+        if (lane < k && (row < 0 || row >= (int32_t)M)) {
+            latch_status(kDevBadIndex);
+            row = -1;
         }
         const float amax = max8(amax16(a, b));
         uint8_t* qb = q + kb * 128 + 16 * sub;
@@ -1231,7 +1258,7 @@ __device__ __forceinline__ float2 sigmoid2(float2 x)
 }
 
 template <bool CKPT>
-__global__ void __launch_bounds__(256, 4) swiglu_quant_kernel(const uint16_t* __restrict__ h, uint32_t M, uint32_t I,
+__global__ void __launch_bounds__(256, 3) swiglu_quant_kernel(const uint16_t* __restrict__ h, uint32_t M, uint32_t I,
                                                               uint32_t rows, uint8_t* __restrict__ q,
                                                               float* __restrict__ s, uint8_t* __restrict__ hq,
                                                               float* __restrict__ hs)
@@ -1249,13 +1276,21 @@ __global__ void __launch_bounds__(256, 4) swiglu_quant_kernel(const uint16_t* __
         uint8_t* qa = q + (size_t)m0 * I + ib * 128 + 16 * sub;
         uint8_t* qh = CKPT ? hq + (size_t)m0 * 2 * I + ib * 128 + 16 * sub : nullptr;
         float sa = 0.0f, sg = 0.0f, su = 0.0f;   // lane sub: the scales of row m0 + sub
-        for (uint32_t i = 0; i < n; ++i, src += 2 * I, qa += I, qh += CKPT ? 2 * I : 0) {
-            uint4 g0 = make_uint4(0u, 0u, 0u, 0u), g1 = g0, u0 = g0, u1 = g0;
-            if (live) {
-                g0 = __ldg(reinterpret_cast<const uint4*>(src));
-                g1 = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-                u0 = __ldg(reinterpret_cast<const uint4*>(src + I));
-                u1 = __ldg(reinterpret_cast<const uint4*>(src + I) + 1);
+        uint4 g0 = make_uint4(0u, 0u, 0u, 0u), g1 = g0, u0 = g0, u1 = g0;
+        if (live) {
+            g0 = __ldg(reinterpret_cast<const uint4*>(src));
+            g1 = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+            u0 = __ldg(reinterpret_cast<const uint4*>(src + I));
+            u1 = __ldg(reinterpret_cast<const uint4*>(src + I) + 1);
+        }
+        uint4 h0 = g0, h1 = g0, v0 = g0, v1 = g0;   // the next row's, loaded while this one is worked on
+        for (uint32_t i = 0; i < n; ++i, qa += I, qh += CKPT ? 2 * I : 0, g0 = h0, g1 = h1, u0 = v0, u1 = v1) {
+            src += 2 * I;
+            if (live && i + 1 < n) {
+                h0 = __ldg(reinterpret_cast<const uint4*>(src));
+                h1 = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+                v0 = __ldg(reinterpret_cast<const uint4*>(src + I));
+                v1 = __ldg(reinterpret_cast<const uint4*>(src + I) + 1);
             }
             float a[16];
             const uint32_t gw[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
