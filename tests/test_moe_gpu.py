@@ -232,7 +232,8 @@ def same_bits(got, want, what):
 
 @pytest.mark.parametrize("weighted", [False, True])
 @pytest.mark.parametrize("T,k,E,C", [(1, 1, 1, 128), (1, 8, 256, 384), (37, 8, 16, 256), (300, 2, 3, 640),
-                                     (129, 1, 5, 128), (64, 32, 40, 256), (513, 3, 1024, 128)])
+                                     (129, 1, 5, 128), (64, 32, 40, 256), (513, 3, 1024, 128),
+                                     (40, 11, 30, 896), (33, 31, 31, 128), (200, 5, 9, 1152)])
 def test_dispatch_is_the_quantisers_of_the_gathered_rows(T, k, E, C, weighted):
     rng = np.random.default_rng(T * k)
     idx = _moe.distinct(rng, T, k, E)
@@ -635,3 +636,118 @@ def test_a_single_token_through_the_layer():
         h = layer.w1[e][1] @ layer.xv[0]
         want[0] += host(w)[0, j] * (layer.w2[e][1] @ _moe.swiglu(h[None])[0])
     assert np.linalg.norm(out - want) <= 0.153 * np.linalg.norm(want)
+
+
+def test_two_layers_on_two_streams_at_once():
+    layers = [Layer(T=300, seed=s) for s in (21, 22)]
+    want = [l.step() for l in layers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    got = [[], []]
+    for _ in range(3):
+        for i, (l, st) in enumerate(zip(layers, streams)):
+            with torch.cuda.stream(st):
+                got[i].append(l.step())
+    torch.cuda.synchronize()
+    ok()
+    for i in range(2):
+        for g in got[i]:
+            for name, v in want[i].items():
+                assert torch.equal(v, g[name]), name
+
+
+FIRST_USE = """
+import torch
+from fp8_fine_grained_fp8q_b200 import ops
+x = torch.randn(130, 256, device="cuda").to(torch.bfloat16)
+logits, bias = torch.randn(130, 16, device="cuda"), torch.zeros(16, device="cuda")
+h, dw = torch.randn(520, 512, device="cuda").to(torch.bfloat16), torch.randn(130, 4, device="cuda")
+
+def step():
+    idx, w = ops.moe_route(logits, 4, bias=bias, n_group=4, topk_group=2)
+    plan = ops.moe_plan(idx, 16)
+    q = ops.moe_dispatch(x, plan, weights=w, transposed=True)
+    a = ops.swiglu_quant(h)
+    b = ops.swiglu_backward_quant(h[:, :256].contiguous(), a[2], a[3], offsets=plan.offsets)
+    y = h[:, 256:].contiguous()
+    out = ops.moe_combine(y, plan, weights=w, add=x)
+    d = ops.moe_route_backward(ops.moe_combine_dweight(out, y, plan), w, idx, logits)
+    return [idx, w, *plan, *q[:2], *a, *b[:2], out, d]
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    captured = step()
+g.replay()
+torch.cuda.synchronize()
+assert ops.device_status() == ops.DEV_OK
+assert all(torch.equal(p, q) for p, q in zip(captured, step()))
+print("same")
+"""
+
+
+def test_first_use_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_USE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
+# -- sizes whose offsets pass 32 bits, against the library's own quantisers ------------------------------ #
+
+def test_dispatch_and_combine_past_32_bit_offsets():
+    T, k, E, C = 70001, 8, 12, 7680                       # 4.3e9 codes in each form
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, C, generator=g, device="cuda", dtype=torch.bfloat16)
+    idx = torch.rand(T, E, generator=g, device="cuda").topk(k).indices.to(torch.int32)
+    plan = ops.moe_plan(idx, E)
+    q, s, qt, st = ops.moe_dispatch(x, plan, transposed=True)
+    ok()
+    M = T * k
+    at = torch.cat([torch.arange(512, device="cuda"), torch.arange(M - 640, M, device="cuda")])
+    rows = x[(plan.slots[at] // k).long()].contiguous()
+    wq, ws = ops.act_1x128(rows)
+    assert torch.equal(q[at], wq) and torch.equal(s[:, at], ws)
+    # The last expert's last whole groups, whose columns lie behind all others'.
+    off = plan.offsets.tolist()
+    groups = [-(-(b - a) // 128) for a, b in zip(off[:-1], off[1:])]
+    n = off[E] - off[E - 1]
+    lo = 128 * (n // 128 - 2)
+    rows = x[(plan.slots[off[E - 1] + lo:off[E - 1] + lo + 256] // k).long()].contiguous()
+    wqt, wst = ops.act_128x1_transposed(rows)
+    first = sum(groups[:-1]) + lo // 128
+    assert torch.equal(qt[:, 128 * first:128 * first + 256], wqt) and torch.equal(st[first:first + 2], wst)
+    del qt, st, q, s
+    y = torch.randn(M, C, generator=g, device="cuda", dtype=torch.bfloat16)
+    out = ops.moe_combine(y, plan)
+    dw = ops.moe_combine_dweight(x, y, plan)
+    ok()
+    for t in (0, T // 2, T - 1):
+        r = y[plan.rows[t].long()].double()
+        tol = 2 * (k + 1) * U32 * r.abs().sum(0)
+        assert bool(((out[t].double() - r.sum(0)).abs() <= tol + U16 * (r.sum(0).abs() + tol)).all())
+        p = r * x[t].double()
+        assert bool(((dw[t].double() - p.sum(1)).abs() <= 128 * U32 * p.abs().sum(1)).all())
+
+
+def test_swiglu_past_32_bit_offsets():
+    M, I = 300001, 7296                                    # 4.4e9 codes of the checkpoint
+    g = torch.Generator(device="cuda").manual_seed(2)
+    h = torch.randn(M, 2 * I, generator=g, device="cuda", dtype=torch.bfloat16)
+    q, s, hq, hs = ops.swiglu_quant(h)
+    ok()
+    for lo in (0, M - 200):
+        tq, ts, thq, ths = ops.swiglu_quant(h[lo:lo + 200].contiguous())
+        assert torch.equal(q[lo:lo + 200], tq) and torch.equal(s[:, lo:lo + 200], ts)
+        assert torch.equal(hq[lo:lo + 200], thq) and torch.equal(hs[:, lo:lo + 200], ths)
+    da = h[:, :I].contiguous()
+    del h, q, s
+    dq, ds, dqt, dst, aqt, ast = ops.swiglu_backward_quant(da, hq, hs)
+    ok()
+    lo = 128 * (M // 128 - 1)
+    n = M - lo                                             # a whole group and the last, partial one
+    want = ops.swiglu_backward_quant(da[lo:].contiguous(), hq[lo:].contiguous(), hs[:, lo:].contiguous())
+    got = (dq[lo:], ds[:, lo:], dqt[:, lo:], dst[lo // 128:], aqt[:, lo:], ast[lo // 128:])
+    assert n > 128 and all(torch.equal(a, b) for a, b in zip(got, want))
