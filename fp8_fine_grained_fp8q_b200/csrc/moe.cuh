@@ -32,6 +32,110 @@ __device__ __forceinline__ uint32_t bf16_rn(float x)
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = (uint16_t)bf16_rn(v); }
 
+// ------------------------------------------------------------------------------------------
+// Arithmetic shared by the kernels below
+// ------------------------------------------------------------------------------------------
+// max(m, |a|, |b|), a NaN losing (max.f32 with three inputs).
+__device__ __forceinline__ float max_abs(float m, float a, float b)
+{
+    float r;
+    asm("{.reg .f32 a, b;\n\t"
+        "abs.f32 a, %2;\n\t"
+        "abs.f32 b, %3;\n\t"
+        "max.f32 %0, %1, a, b;}"
+        : "=f"(r)
+        : "f"(m), "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float amax16f(const float (&f)[16])
+{
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) m = max_abs(m, f[i], f[i + 1]);
+    return m;
+}
+// Four codes of four values, the first in the low byte.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d)
+{
+    uint32_t r;
+    asm("{.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float inv)
+{
+    return codes4(__fmul_rn(a, inv), __fmul_rn(b, inv), __fmul_rn(c, inv), __fmul_rn(d, inv));
+}
+__device__ __forceinline__ uint4 quant16f(const float (&f)[16], float inv)
+{
+    return make_uint4(e4m3x4(f[0], f[1], f[2], f[3], inv), e4m3x4(f[4], f[5], f[6], f[7], inv),
+                      e4m3x4(f[8], f[9], f[10], f[11], inv), e4m3x4(f[12], f[13], f[14], f[15], inv));
+}
+// The largest of 8 neighbouring lanes (all 32 take part).
+__device__ __forceinline__ float max8(float v)
+{
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+// Two FP32 products at once (mul.rn.f32x2: each rounded to nearest, as __fmul_rn).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 c, a, b;\n\t"
+        "mov.b64 {%0, %1}, c;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, d;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 c, a, b;\n\t"
+        "mov.b64 {%0, %1}, c;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// Two bf16 values as FP32, by a mixed-precision x + (-0), which is x: it runs on the FMA pipe, whereas
+// shifting and masking take the ALU, which the conversions to E4M3 and the maxima already fill.
+__device__ __forceinline__ float2 widen(uint32_t w)
+{
+    float2 r;
+    asm("{.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "add.f32.bf16 %0, l, %3;\n\t"
+        "add.f32.bf16 %1, h, %3;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(w), "f"(-0.0f));
+    return r;
+}
+
 __device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll
@@ -711,124 +815,6 @@ __device__ __forceinline__ void group_rows(const GroupTable& t, int E, int g, in
 // tiles of one token (eight lanes each), reads them once and writes them to the token's k rows: bound
 // by the writes.  Without weights the k rows hold the same codes, which are formed once.
 // ------------------------------------------------------------------------------------------
-__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&f)[16])
-{
-    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        f[2 * i] = bf16_lo(u[i]);
-        f[2 * i + 1] = bf16_hi(u[i]);
-    }
-}
-// max(m, |a|, |b|), a NaN losing (max.f32 with three inputs).
-__device__ __forceinline__ float max_abs(float m, float a, float b)
-{
-    float r;
-    asm("{.reg .f32 a, b;\n\t"
-        "abs.f32 a, %2;\n\t"
-        "abs.f32 b, %3;\n\t"
-        "max.f32 %0, %1, a, b;}"
-        : "=f"(r)
-        : "f"(m), "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float amax16f(const float (&f)[16])
-{
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) m = max_abs(m, f[i], f[i + 1]);
-    return m;
-}
-// Four codes of four values, the first in the low byte.
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d)
-{
-    uint32_t r;
-    asm("{.reg .b16 l, h;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
-        "mov.b32 %0, {l, h};}"
-        : "=r"(r)
-        : "f"(a), "f"(b), "f"(c), "f"(d));
-    return r;
-}
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float inv)
-{
-    return codes4(__fmul_rn(a, inv), __fmul_rn(b, inv), __fmul_rn(c, inv), __fmul_rn(d, inv));
-}
-__device__ __forceinline__ uint4 quant16f(const float (&f)[16], float inv)
-{
-    return make_uint4(e4m3x4(f[0], f[1], f[2], f[3], inv), e4m3x4(f[4], f[5], f[6], f[7], inv),
-                      e4m3x4(f[8], f[9], f[10], f[11], inv), e4m3x4(f[12], f[13], f[14], f[15], inv));
-}
-// The largest of 8 neighbouring lanes (all 32 take part).
-__device__ __forceinline__ float max8(float v)
-{
-#pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-    return v;
-}
-
-// Two FP32 products at once (mul.rn.f32x2: each rounded to nearest, as __fmul_rn).
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 r;
-    asm("{.reg .b64 a, b, c;\n\t"
-        "mov.b64 a, {%2, %3};\n\t"
-        "mov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 c, a, b;\n\t"
-        "mov.b64 {%0, %1}, c;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 r;
-    asm("{.reg .b64 a, b, c, d;\n\t"
-        "mov.b64 a, {%2, %3};\n\t"
-        "mov.b64 b, {%4, %5};\n\t"
-        "mov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\t"
-        "mov.b64 {%0, %1}, d;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 r;
-    asm("{.reg .b64 a, b, c;\n\t"
-        "mov.b64 a, {%2, %3};\n\t"
-        "mov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 c, a, b;\n\t"
-        "mov.b64 {%0, %1}, c;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-// Two bf16 values as FP32, by a mixed-precision x + (-0), which is x: it runs on the FMA pipe, whereas
-// shifting and masking take the ALU, which the conversions to E4M3 and the maxima already fill.
-__device__ __forceinline__ float2 widen(uint32_t w)
-{
-    float2 r;
-    asm("{.reg .b16 l, h;\n\t"
-        "mov.b32 {l, h}, %2;\n\t"
-        "add.f32.bf16 %0, l, %3;\n\t"
-        "add.f32.bf16 %1, h, %3;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "r"(w), "f"(-0.0f));
-    return r;
-}
-__device__ __forceinline__ uint32_t abs2(uint32_t w) { return w & 0x7FFF7FFFu; }
-// Larger of each of two bf16 pairs; a NaN loses, as in fmaxf.
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 template <bool WEIGHTED>
 __global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* __restrict__ x,
                                                                 const int32_t* __restrict__ rows,

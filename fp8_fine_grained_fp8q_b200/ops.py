@@ -464,11 +464,23 @@ def _launch(entry: str, dev: torch.device, *args):
         raise Fp8qError(entry, status)
 
 
-def _together(dev: torch.device, *named):
-    """Every tensor of (tensor, name, ...) pairs lies on `dev`."""
-    for t, name in named:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, dev: torch.device):
+    """_require, and on `dev`; one test where all is well."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.dim() == ndim and t.is_cuda
+            and t.is_contiguous()):
+        return
+    _require(t, name, dtype, ndim)
+    raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _made(t, name: str, dtype: torch.dtype, dev: torch.device, *shape):
+    """An output: made, or checked as _need and for its shape."""
+    if t is None:
+        return torch.empty(*shape, dtype=dtype, device=dev)
+    _need(t, name, dtype, len(shape), dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return t
 
 
 def _router(logits: torch.Tensor, score: str):
@@ -483,23 +495,23 @@ def _router(logits: torch.Tensor, score: str):
 def _plan(plan: MoePlan, dev: torch.device):
     """Checked (T, k, E) of a plan."""
     offsets, slots, rows = plan
-    _require(offsets, "plan.offsets", torch.int32, 1)
-    _require(slots, "plan.slots", torch.int32, 1)
-    _require(rows, "plan.rows", torch.int32, 2)
-    _together(dev, (offsets, "plan.offsets"), (slots, "plan.slots"), (rows, "plan.rows"))
-    if slots.numel() != rows.numel():
+    _need(offsets, "plan.offsets", torch.int32, 1, dev)
+    _need(slots, "plan.slots", torch.int32, 1, dev)
+    _need(rows, "plan.rows", torch.int32, 2, dev)
+    T, k = rows.shape
+    E = offsets.shape[0] - 1
+    if slots.shape[0] != T * k:
         raise ValueError("plan.slots and plan.rows must have the same number of entries")
-    if offsets.numel() < 2:
+    if E < 1:
         raise ValueError("plan.offsets must have E+1 entries")
-    return rows.shape[0], rows.shape[1], offsets.numel() - 1
+    return T, k, E
 
 
 def _weights(weights, T: int, k: int, dev: torch.device):
     if weights is not None:
-        _require(weights, "weights", torch.float32, 2)
-        if tuple(weights.shape) != (T, k):
+        _need(weights, "weights", torch.float32, 2, dev)
+        if weights.shape != (T, k):
             raise ValueError(f"weights must have shape {(T, k)}, got {tuple(weights.shape)}")
-        _together(dev, (weights, "weights"))
 
 
 def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None, score: str = "sigmoid",
@@ -514,14 +526,13 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None
     T, E = logits.shape
     dev = logits.device
     if bias is not None:
-        _require(bias, "bias", torch.float32, 1)
-        if bias.numel() != E:
+        _need(bias, "bias", torch.float32, 1, dev)
+        if bias.shape[0] != E:
             raise ValueError(f"bias must have {E} entries, got {bias.numel()}")
     if top_k < 1:
         raise ValueError("top_k must be at least 1")
-    idx = _out(idx, (T, top_k), torch.int32, dev, "idx")
-    w = _out(w, (T, top_k), torch.float32, dev, "w")
-    _together(dev, (bias, "bias"), (idx, "idx"), (w, "w"))
+    idx = _made(idx, "idx", torch.int32, dev, T, top_k)
+    w = _made(w, "w", torch.float32, dev, T, top_k)
     _launch("fp8q_moe_route", dev, _at(logits), kind, _at(bias), T, E, top_k, n_group, topk_group, fn,
             int(renormalize), scale, _at(idx), _at(w))
     return idx, w
@@ -535,14 +546,14 @@ def moe_route_backward(dw: torch.Tensor, w: torch.Tensor, idx: torch.Tensor, log
     kind, fn = _router(logits, score)
     T, E = logits.shape
     dev = logits.device
-    _require(idx, "idx", torch.int32, 2)
+    _need(idx, "idx", torch.int32, 2, dev)
     k = idx.shape[1]
-    for t, name, dtype in ((dw, "dw", torch.float32), (w, "w", torch.float32), (idx, "idx", torch.int32)):
-        _require(t, name, dtype, 2)
-        if tuple(t.shape) != (T, k):
-            raise ValueError(f"{name} must have shape {(T, k)}, got {tuple(t.shape)}")
-    out = _out(out, (T, E), logits.dtype, dev, "out")
-    _together(dev, (dw, "dw"), (w, "w"), (idx, "idx"), (out, "out"))
+    _need(dw, "dw", torch.float32, 2, dev)
+    _need(w, "w", torch.float32, 2, dev)
+    if not idx.shape == dw.shape == w.shape == (T, k):
+        raise ValueError(f"dw, w and idx must have shape {(T, k)}, got {tuple(dw.shape)}, {tuple(w.shape)} and "
+                         f"{tuple(idx.shape)}")
+    out = _made(out, "out", logits.dtype, dev, T, E)
     _launch("fp8q_moe_route_backward", dev, _at(dw), _at(w), _at(idx), _at(logits), kind, T, E, k, fn,
             int(renormalize), scale, _at(out))
     return out
@@ -555,10 +566,9 @@ def moe_plan(idx: torch.Tensor, E: int, offsets: torch.Tensor | None = None, slo
     _require(idx, "idx", torch.int32, 2)
     T, k = idx.shape
     dev = idx.device
-    offsets = _out(offsets, (E + 1,), torch.int32, dev, "offsets")
-    slots = _out(slots, (T * k,), torch.int32, dev, "slots")
-    rows = _out(rows, (T, k), torch.int32, dev, "rows")
-    _together(dev, (offsets, "offsets"), (slots, "slots"), (rows, "rows"))
+    offsets = _made(offsets, "offsets", torch.int32, dev, E + 1)
+    slots = _made(slots, "slots", torch.int32, dev, T * k)
+    rows = _made(rows, "rows", torch.int32, dev, T, k)
     _launch("fp8q_moe_plan", dev, _at(idx), T, k, E, _at(offsets), _at(slots), _at(rows))
     return MoePlan(offsets, slots, rows)
 
@@ -578,13 +588,12 @@ def moe_dispatch(x: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None = 
         raise ValueError(f"x has {Tx} tokens, the plan {T}")
     _weights(weights, T, k, dev)
     M = T * k
-    q = _out(q, (M, C), torch.uint8, dev, "q")
-    s = _out(s, (C // 128, M), torch.float32, dev, "s")
+    q = _made(q, "q", torch.uint8, dev, M, C)
+    s = _made(s, "s", torch.float32, dev, C // 128, M)
     if transposed or qt is not None or st is not None:
         Kcap = ragged_capacity(M, E) if Kcap is None else Kcap
-        qt = _out(qt, (C, Kcap), torch.uint8, dev, "qt")
-        st = _out(st, (Kcap // 128, C), torch.float32, dev, "st")
-    _together(dev, (q, "q"), (s, "s"), (qt, "qt"), (st, "st"))
+        qt = _made(qt, "qt", torch.uint8, dev, C, Kcap)
+        st = _made(st, "st", torch.float32, dev, Kcap // 128, C)
     _launch("fp8q_moe_dispatch", dev, _at(x), _at(plan.offsets), _at(plan.slots), _at(plan.rows), _at(weights), E, T, k, C,
             _at(q), _at(s), _at(qt), _at(st), Kcap or 0)
     return q, s, qt, st
@@ -602,9 +611,8 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None = N
         raise ValueError(f"y has {M} rows, the plan {T * k}")
     _weights(weights, T, k, dev)
     if add is not None:
-        add = _out(add, (T, C), torch.bfloat16, dev, "add")
-    out = _out(out, (T, C), torch.bfloat16, dev, "out")
-    _together(dev, (add, "add"), (out, "out"))
+        add = _made(add, "add", torch.bfloat16, dev, T, C)
+    out = _made(out, "out", torch.bfloat16, dev, T, C)
     _launch("fp8q_moe_combine", dev, _at(y), _at(plan.rows), _at(weights), _at(add), T, k, C, _at(out))
     return out
 
@@ -612,14 +620,13 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None = N
 def moe_combine_dweight(dout: torch.Tensor, y: torch.Tensor, plan: MoePlan, out: torch.Tensor | None = None):
     """Gradient of moe_combine's weights: dw[T,k] fp32, dw[t,j] = <dout[t], y[rows[t,j]]>."""
     _require(dout, "dout", torch.bfloat16, 2)
-    _require(y, "y", torch.bfloat16, 2)
     dev = dout.device
+    _need(y, "y", torch.bfloat16, 2, dev)
     T, k, _ = _plan(plan, dev)
     C = dout.shape[1]
     if dout.shape[0] != T or tuple(y.shape) != (T * k, C):
         raise ValueError(f"dout must be [{T}, C] and y [{T * k}, C], got {tuple(dout.shape)} and {tuple(y.shape)}")
-    out = _out(out, (T, k), torch.float32, dev, "out")
-    _together(dev, (y, "y"), (out, "out"))
+    out = _made(out, "out", torch.float32, dev, T, k)
     _launch("fp8q_moe_combine_dweight", dev, _at(dout), _at(y), _at(plan.rows), T, k, C, _at(out))
     return out
 
@@ -635,12 +642,11 @@ def swiglu_quant(h: torch.Tensor, checkpoint: bool = True, q: torch.Tensor | Non
     if two % 2:
         raise ValueError(f"h must have an even number of columns, got {two}")
     I = two // 2
-    q = _out(q, (M, I), torch.uint8, dev, "q")
-    s = _out(s, (I // 128, M), torch.float32, dev, "s")
+    q = _made(q, "q", torch.uint8, dev, M, I)
+    s = _made(s, "s", torch.float32, dev, I // 128, M)
     if checkpoint or hq is not None or hs is not None:
-        hq = _out(hq, (M, two), torch.uint8, dev, "hq")
-        hs = _out(hs, (two // 128, M), torch.float32, dev, "hs")
-    _together(dev, (q, "q"), (s, "s"), (hq, "hq"), (hs, "hs"))
+        hq = _made(hq, "hq", torch.uint8, dev, M, two)
+        hs = _made(hs, "hs", torch.float32, dev, two // 128, M)
     _launch("fp8q_swiglu_quant", dev, _at(h), M, I, _at(q), _at(s), _at(hq), _at(hs))
     return q, s, hq, hs
 
@@ -655,27 +661,25 @@ def swiglu_backward_quant(da: torch.Tensor, hq: torch.Tensor, hs: torch.Tensor, 
     expert (as act_128x1_transposed_ragged); without them they are one sequence, padded to Kcap =
     the next multiple of 128."""
     _require(da, "da", torch.bfloat16, 2)
-    _require(hq, "hq", torch.uint8, 2)
-    _require(hs, "hs", torch.float32, 2)
     M, I = da.shape
     dev = da.device
+    _need(hq, "hq", torch.uint8, 2, dev)
+    _need(hs, "hs", torch.float32, 2, dev)
     if tuple(hq.shape) != (M, 2 * I) or tuple(hs.shape) != (2 * I // 128, M):
         raise ValueError(f"the checkpoint of [{M}, {2 * I}] has codes {(M, 2 * I)} and scales {(2 * I // 128, M)}, "
                          f"got {tuple(hq.shape)} and {tuple(hs.shape)}")
     E = 1
     if offsets is not None:
-        _require(offsets, "offsets", torch.int32, 1)
-        E = offsets.numel() - 1
+        _need(offsets, "offsets", torch.int32, 1, dev)
+        E = offsets.shape[0] - 1
     if Kcap is None:
         Kcap = 128 * ((M + 127) // 128) if offsets is None else ragged_capacity(M, E)
-    q = _out(q, (M, 2 * I), torch.uint8, dev, "q")
-    s = _out(s, (2 * I // 128, M), torch.float32, dev, "s")
-    qt = _out(qt, (2 * I, Kcap), torch.uint8, dev, "qt")
-    st = _out(st, (Kcap // 128, 2 * I), torch.float32, dev, "st")
-    aqt = _out(aqt, (I, Kcap), torch.uint8, dev, "aqt")
-    ast = _out(ast, (Kcap // 128, I), torch.float32, dev, "ast")
-    _together(dev, (hq, "hq"), (hs, "hs"), (offsets, "offsets"), (q, "q"), (s, "s"), (qt, "qt"), (st, "st"),
-              (aqt, "aqt"), (ast, "ast"))
+    q = _made(q, "q", torch.uint8, dev, M, 2 * I)
+    s = _made(s, "s", torch.float32, dev, 2 * I // 128, M)
+    qt = _made(qt, "qt", torch.uint8, dev, 2 * I, Kcap)
+    st = _made(st, "st", torch.float32, dev, Kcap // 128, 2 * I)
+    aqt = _made(aqt, "aqt", torch.uint8, dev, I, Kcap)
+    ast = _made(ast, "ast", torch.float32, dev, Kcap // 128, I)
     _launch("fp8q_swiglu_backward_quant", dev, _at(da), _at(hq), _at(hs), _at(offsets), E, M, I, _at(q), _at(s), _at(qt),
             _at(st), _at(aqt), _at(ast), Kcap)
     return q, s, qt, st, aqt, ast
