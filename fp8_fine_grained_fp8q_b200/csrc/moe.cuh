@@ -1225,9 +1225,10 @@ __global__ void __launch_bounds__(256) moe_combine_dweight_kernel(const uint16_t
 // SwiGLU: a = silu(g) u with g = h[:, :I], u = h[:, I:], quantised from FP32; with `hq`, the 1x128
 // codes of h itself are the checkpoint that the backward pass starts from.  Eight lanes own one
 // 128-element tile of a (and the two tiles of h that it comes from), a warp four neighbouring tiles of
-// `rows` rows, one row after another: with eight rows, the scales of a tile column leave as whole
-// 32-byte sectors.  One lane of the eight forms each of the three scales.
-// Bound by HBM; the two MUFU operations an element take 60 us of 65536 x 2048, the bytes 145.
+// `rows` rows, one row after another, the next one's loads in flight: with eight rows, the scales of a
+// tile column leave as whole 32-byte sectors.  One lane of the eight forms each of the three scales.
+// Bound by HBM: 65536 x 2048 with the checkpoint takes 158 us, 6.0 TB/s (the two MUFU operations an
+// element alone would take 60 us).  Two CTAs an SM with 110 registers; three with 80 spill: 176 us.
 // ------------------------------------------------------------------------------------------
 // sigmoid of two values by ex2 and a fast reciprocal: with the rounding of x log2 e, a relative error below
 // (4 + 1.5 |x|) 2^-24 and a few steps of the two functions; beyond |x| = 88 the result is 0 or 1.
@@ -1244,7 +1245,7 @@ __device__ __forceinline__ float2 sigmoid2(float2 x)
 }
 
 template <bool CKPT>
-__global__ void __launch_bounds__(256, 3) swiglu_quant_kernel(const uint16_t* __restrict__ h, uint32_t M, uint32_t I,
+__global__ void __launch_bounds__(256, 2) swiglu_quant_kernel(const uint16_t* __restrict__ h, uint32_t M, uint32_t I,
                                                               uint32_t rows, uint8_t* __restrict__ q,
                                                               float* __restrict__ s, uint8_t* __restrict__ hq,
                                                               float* __restrict__ hs)
