@@ -94,16 +94,17 @@ int launch_route(const void* logits, const float* bias, int64_t T, int E, int k,
 #undef FP8Q_ROUTE
 }
 
-template <typename L, bool SOFTMAX>
+template <typename L, bool DENSE>
 int launch_route_backward(const float* dw, const float* w, const int32_t* idx, const void* logits, int64_t T, int E,
-                          int k, int renorm, float scale, void* dlogits, cudaStream_t st)
+                          int k, int sigmoid, int renorm, float scale, void* dlogits, cudaStream_t st)
 {
     const dim3 grid((unsigned)((T + 3) / 4));
     const L* l = static_cast<const L*>(logits);
     L* d = static_cast<L*>(dlogits);
-#define FP8Q_ROUTE(NV)                                                                                              \
-    return launch_kernel(moe_route_backward_kernel<L, NV, SOFTMAX>, grid, dim3(128), 0, st, false, dw, w, idx, l, T, \
-                         E, k, renorm, scale, d)
+    const bool wide = E % 8 == 0 && aligned16(logits) && aligned16(dlogits);
+#define FP8Q_ROUTE(NV)                                                                                             \
+    return launch_kernel(moe_route_backward_kernel<L, NV, DENSE>, grid, dim3(128), 0, st, false, dw, w, idx, l, T, E, \
+                         k, wide, sigmoid, renorm, scale, d)
     if (E <= 32) FP8Q_ROUTE(1);
     if (E <= 64) FP8Q_ROUTE(2);
     if (E <= 128) FP8Q_ROUTE(4);
@@ -162,11 +163,10 @@ int fp8q_moe_route_backward(const float* dw, const float* w, const int32_t* idx,
     const uintptr_t both = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits);
     if ((both & (bf16 ? 1u : 3u)) != 0 || !aligned4(dw) || !aligned4(w) || !aligned4(idx)) return FP8Q_ERR_ALIGN;
     const cudaStream_t st = (cudaStream_t)stream;
-    const bool softmax = score == FP8Q_SCORE_SOFTMAX;
-    const auto launch =
-        bf16 ? (softmax ? launch_route_backward<uint16_t, true> : launch_route_backward<uint16_t, false>)
-             : (softmax ? launch_route_backward<float, true> : launch_route_backward<float, false>);
-    return launch(dw, w, idx, logits, T, E, k, renormalize != 0, scale, dlogits, st);
+    const bool sigmoid = score == FP8Q_SCORE_SIGMOID, dense = !sigmoid && renormalize == 0;
+    const auto launch = bf16 ? (dense ? launch_route_backward<uint16_t, true> : launch_route_backward<uint16_t, false>)
+                             : (dense ? launch_route_backward<float, true> : launch_route_backward<float, false>);
+    return launch(dw, w, idx, logits, T, E, k, sigmoid, renormalize != 0, scale, dlogits, st);
 }
 
 int fp8q_moe_plan(const int32_t* idx, int64_t T, int32_t k, int32_t E, int32_t* offsets, int32_t* slots,

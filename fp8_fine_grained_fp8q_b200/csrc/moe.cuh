@@ -156,10 +156,10 @@ __device__ __forceinline__ T warp_sum(T v)
 // which is the same order and needs no arithmetic); equal keys go to the lower index.  A masked
 // expert (logit or bias -inf, NaN or +inf) has the key -inf.
 //
-// Keys are first formed in binary32, whose error is bounded below.  Where two neighbours in the order
-// found that way (or the groups on the two sides of the border) are nearer than the bound, the token is
-// done again with keys in binary64; that is rare, and it costs the few tokens about 3 us.  With
-// binary64 throughout, 8192 tokens of 256 experts took 65 us instead of 11.
+// Keys are first formed in binary32 and truncated, with an error that is bounded below.  Where two
+// neighbours in the order found that way (or the groups on the two sides of the border) are nearer than
+// the bound, the token is done again with whole keys, in binary64 where there is a bias; that is rare.
+// MEASURED
 // Bound by latency and instruction issue; the logits are 8 MB.
 // ------------------------------------------------------------------------------------------
 // Keys as unsigned integers of the same order, above 1.  0: not to be chosen (again); 1: masked.
@@ -197,12 +197,9 @@ struct RouteShape {
 };
 
 // Lane j: the j-th expert by key[i] (of expert lane * NV + i; -inf: masked).  `pair`: a group's score is
-// the sum of its two largest keys, not its largest.  near, near_group: where the keys of two neighbours
-// (the scores of the groups at the border) are not further apart, and not from the same logit and bias,
-// *unsure is set; negative: the keys are exact.
-template <typename F, int NV, typename Same>
-__device__ __forceinline__ int choose(const F (&key)[NV], const RouteShape& sh, bool pair, F near, F near_group,
-                                      Same same, bool* unsure)
+// the sum of its two largest keys, not its largest.
+template <typename F, int NV>
+__device__ __forceinline__ int choose(const F (&key)[NV], const RouteShape& sh, bool pair)
 {
     typedef typename Rank<F>::type R;
     const int lane = threadIdx.x & 31, e0 = lane * NV;
@@ -237,11 +234,6 @@ __device__ __forceinline__ int choose(const F (&key)[NV], const RouteShape& sh, 
         }
         if (lane >= sh.n_group) rank = 32;
         allowed = __ballot_sync(kFull, rank < sh.topk_group);
-        if (pair && near_group >= (F)0) {
-            const F in = __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, rank == sh.topk_group - 1)) - 1);
-            const F out = __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, rank == sh.topk_group)) - 1);
-            if (out > lowest<F>() && !(in - out > near_group)) *unsure = true;
-        }
     }
     R rank[NV];
     int g = e0 / per, left = per - (e0 - g * per);   // the group at hand, and its experts from here on
@@ -258,22 +250,15 @@ __device__ __forceinline__ int choose(const F (&key)[NV], const RouteShape& sh, 
     R best = 0;   // of this lane
 #pragma unroll
     for (int i = 0; i < NV; ++i) best = best > rank[i] ? best : rank[i];
-    int chosen = 0, last_e = -1;
-    F last = lowest<F>();
-    const bool check = near >= (F)0;
-    const int rounds = check && sh.topk_group * per > sh.k ? sh.k + 1 : sh.k;
-    for (int j = 0; j < rounds; ++j) {
+    int chosen = 0;
+    for (int j = 0; j < sh.k; ++j) {
         const R top = warp_top(best);
         const int who = __ffs(__ballot_sync(kFull, best == top)) - 1;   // the lowest lane has the lowest index
         int at = 0;
-        F value = lowest<F>();
         if (lane == who) {
 #pragma unroll
             for (int i = NV - 1; i >= 0; --i)
-                if (rank[i] == top) {
-                    at = i;
-                    value = key[i];
-                }
+                if (rank[i] == top) at = i;
             best = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -282,9 +267,121 @@ __device__ __forceinline__ int choose(const F (&key)[NV], const RouteShape& sh, 
             }
         }
         const int e = __shfl_sync(kFull, e0 + at, who);
-        if (check) {
-            value = __shfl_sync(kFull, value, who);
-            if (j > 0 && value > lowest<F>() && !(last - value > near)) {
+        if (lane == j) chosen = e;
+    }
+    return chosen;
+}
+
+// The same choice from truncated keys, in about a third of the instructions: the low bits of a key's rank
+// hold its place in the lane (the lowest index the highest), so a lane's keys sort as plain integers
+// and the winner carries its index.  Ties of truncated keys go to the lower index; the border conditions
+// below make sure that the order found is that of the keys before truncation, or set *unsure.
+// Batcher's odd-even merge sort, descending.
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&r)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t hi = max(r[i + j], r[i + j + q]), lo = min(r[i + j], r[i + j + q]);
+                        r[i + j] = hi;
+                        r[i + j + q] = lo;
+                    }
+}
+
+__device__ __forceinline__ float key_of(uint32_t rank)   // of a rank above 1
+{
+    return __uint_as_float(rank ^ ((rank >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// exact: truncation loses nothing (bf16 logits without a bias), so that ties are ties.
+template <int NV, typename Same>
+__device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteShape& sh, bool pair, bool exact,
+                                           float near, float near_group, Same same, bool* unsure)
+{
+    constexpr uint32_t kPlace = NV - 1;   // NV is a power of two
+    const int lane = threadIdx.x & 31, e0 = lane * NV;
+    const int per = sh.E / sh.n_group;
+    // Masked: the lowest ranks there are, in the order of the index; an expert that is not there: 0.
+    uint32_t rank[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const uint32_t r = key[i] > -CUDART_INF_F ? rank_of(key[i]) & ~kPlace : NV;   // a finite key's is above 2^23
+        rank[i] = e0 + i < sh.E ? r | (kPlace - (uint32_t)i) : 0u;
+    }
+    const auto value_of = [](uint32_t r) { return r >= 2u * NV ? key_of(r & ~kPlace) : -CUDART_INF_F; };
+
+    const int seg = per / NV;
+    const bool whole = seg * NV == per && (seg & (seg - 1)) == 0;   // a group is a power of two of whole lanes
+    const bool grouped = sh.n_group > sh.topk_group;
+    // Up to eight keys are sorted; longer lists cost more to sort than to search.
+    if (NV <= 8 && (whole || !grouped)) sort_down<NV>(rank);
+    if (grouped) {
+        float mine = -CUDART_INF_F;   // lane g: the score of group g
+        if (whole) {
+            float a = -CUDART_INF_F, b = -CUDART_INF_F;
+            if (NV <= 8) {
+                a = value_of(rank[0]);
+                if (NV > 1) b = value_of(rank[NV > 1 ? 1 : 0]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) merge_two(a, b, key[i], -CUDART_INF_F);
+            }
+            for (int o = 1; o < seg; o <<= 1) merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
+            mine = __shfl_sync(kFull, pair && b > -CUDART_INF_F ? a + b : a, (lane * seg) & 31);
+        } else {
+            for (int g = 0; g < sh.n_group; ++g) {
+                float a = -CUDART_INF_F, b = -CUDART_INF_F;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (e0 + i >= g * per && e0 + i < (g + 1) * per) merge_two(a, b, key[i], -CUDART_INF_F);
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1)
+                    merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
+                if (lane == g) mine = pair && b > -CUDART_INF_F ? a + b : a;
+            }
+        }
+        int place = 0;
+        for (int g = 0; g < sh.n_group; ++g) {
+            const float other = __shfl_sync(kFull, mine, g);
+            if (other > mine || (other == mine && g < lane)) ++place;
+        }
+        if (lane >= sh.n_group) place = 32;
+        const uint32_t allowed = __ballot_sync(kFull, place < sh.topk_group);
+        if (!exact) {
+            const float in = __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, place == sh.topk_group - 1)) - 1);
+            const float out = __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, place == sh.topk_group)) - 1);
+            if (out > -CUDART_INF_F && !(in - out > near_group)) *unsure = true;
+        }
+        // Experts of the other groups are out.  (rank holds its place, so it may be sorted already.)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int g = whole ? lane / seg : (e0 + (int)(kPlace - (rank[i] & kPlace))) / per;
+            if (!((allowed >> (g & 31)) & 1u)) rank[i] = 0u;
+        }
+        if (NV <= 8 && !whole) sort_down<NV>(rank);
+    }
+    uint32_t head = rank[0];
+    if (NV > 8) {
+#pragma unroll
+        for (int i = 1; i < NV; ++i) head = max(head, rank[i]);
+    }
+    int chosen = 0, last_e = 0;
+    float last = CUDART_INF_F;
+    const int rounds = !exact && sh.topk_group * per > sh.k ? sh.k + 1 : sh.k;
+    for (int j = 0; j < rounds; ++j) {
+        const uint32_t top = __reduce_max_sync(kFull, head & ~kPlace);
+        const int who = __ffs(__ballot_sync(kFull, (head & ~kPlace) == top)) - 1;   // the lowest lane: the lowest index
+        const int e = __shfl_sync(kFull, e0 + (int)(kPlace - (head & kPlace)), who);
+        if (!exact) {
+            const float value = value_of(top);
+            if (j > 0 && value > -CUDART_INF_F && !(last - value > near)) {
                 // Equal inputs have equal keys; at the border an equal neighbour may hide the next one.
                 if (j == sh.k || !same(last_e, e)) *unsure = true;
             }
@@ -292,6 +389,22 @@ __device__ __forceinline__ int choose(const F (&key)[NV], const RouteShape& sh, 
             last_e = e;
         }
         if (lane == j) chosen = e;   // (round k is for the check only)
+        if (NV <= 8) {
+            if (lane == who) {
+#pragma unroll
+                for (int i = 0; i + 1 < NV; ++i) rank[i] = rank[i + 1];
+                rank[NV - 1] = 0u;
+            }
+            head = rank[0];
+        } else if (lane == who) {
+            uint32_t best = 0u;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (rank[i] == head) rank[i] = 0u;
+                best = max(best, rank[i]);
+            }
+            head = best;
+        }
     }
     return chosen;
 }
@@ -370,12 +483,13 @@ __device__ __forceinline__ void load_route(RouteRow<L, NV>& r, const L* row, con
     r.top = warp_max(top);
 }
 
-// The choice with keys in binary64; only ever with a bias.
+// The choice from whole keys: the logits, or with a bias binary64 sums.
 template <typename L, int NV, bool SOFTMAX>
 __device__ __noinline__ int choose_exactly(const L* row, const float* bias, RouteShape sh, bool wide)
 {
     RouteRow<L, NV> r;
     load_route<L, NV>(r, row, bias, sh.E, wide);
+    if (!bias) return choose<float, NV>(r.l, sh, false);
     double key[NV], total = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -389,8 +503,7 @@ __device__ __noinline__ int choose_exactly(const L* row, const float* bias, Rout
         if (SOFTMAX) key[i] = key[i] / total;
         key[i] = r.l[i] > -CUDART_INF_F && r.b[i] > -CUDART_INF_F ? key[i] + (double)r.b[i] : -CUDART_INF;
     }
-    bool unsure = false;
-    return choose<double, NV>(key, sh, true, -1.0, -1.0, [](int, int) { return true; }, &unsure);
+    return choose<double, NV>(key, sh, true);
 }
 
 template <typename L, int NV, bool SOFTMAX>
@@ -421,27 +534,28 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ lo
         }
         if (SOFTMAX) total = warp_sum(total);
     }
-    int chosen;
-    if (!bias) {
-        bool unsure = false;
-        chosen = choose<float, NV>(r.l, sh, false, -1.0f, -1.0f, [](int, int) { return true; }, &unsure);
-    } else {
-        float largest = 0.0f;
-        const float inv = SOFTMAX ? __fdividef(1.0f, total) : 1.0f;
+    // Truncation takes less than NV steps off a key, each at most 2^-23 of the largest key, or 2^-149.
+    constexpr float kCut = NV * 0x1p-23f;
+    const bool exact = !bias && sizeof(L) == 2;
+    float largest = 0.0f, near = 0.0f;
+    const float inv = SOFTMAX ? __fdividef(1.0f, total) : 1.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool usable = r.l[i] > -CUDART_INF_F && r.b[i] > -CUDART_INF_F;
-            key[i] = usable ? (SOFTMAX ? key[i] * inv : key[i]) + r.b[i] : -CUDART_INF_F;
-            if (usable) largest = fmaxf(largest, fabsf(key[i]));
-        }
-        largest = warp_max(largest);
-        const float near = (SOFTMAX ? 0x1p-16f : 0x1p-20f) + 0x1p-22f * largest;
-        bool unsure = false;
-        chosen = choose<float, NV>(key, sh, true, near, 4.0f * near,
-                                   [&](int p, int q) { return load_logit(row + p) == load_logit(row + q) && bias[p] == bias[q]; },
-                                   &unsure);
-        if (unsure) chosen = choose_exactly<L, NV, SOFTMAX>(row, bias, sh, wide);   // the same for the whole warp
+    for (int i = 0; i < NV; ++i) {
+        if (bias)
+            key[i] = r.l[i] > -CUDART_INF_F && r.b[i] > -CUDART_INF_F ? (SOFTMAX ? key[i] * inv : key[i]) + r.b[i] : -CUDART_INF_F;
+        else
+            key[i] = r.l[i];
+        if (key[i] > -CUDART_INF_F) largest = fmaxf(largest, fabsf(key[i]));
     }
+    if (!exact) {
+        largest = warp_max(largest);
+        near = (bias ? (SOFTMAX ? 0x1p-16f : 0x1p-20f) + 0x1p-22f * largest : 0.0f) + 2.0f * kCut * largest + 4 * NV * 0x1p-149f;
+    }
+    bool unsure = false;
+    int chosen = choose_fast<NV>(key, sh, bias != nullptr, exact, near, 4.0f * near,
+                                 [&](int p, int q) { return load_logit(row + p) == load_logit(row + q) && (!bias || bias[p] == bias[q]); },
+                                 &unsure);
+    if (unsure) chosen = choose_exactly<L, NV, SOFTMAX>(row, bias, sh, wide);   // the same for the whole warp
 
     // Weights.  The renormalised ones divide scores by their sum, so scores that would underflow are
     // first scaled by exp(-m), m = min(largest chosen logit, 0): sigmoid(l) e^-m = e^(l-m) / (1 + e^l).
@@ -476,13 +590,46 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ lo
 //   as they are:   sigmoid  dl_j = w_j (1 - s_j) g_j                       softmax dl_e = [chosen] w_e g_e - p_e sum_i w_i g_i
 // (sum_i p_i = 1 turns g_j - sum_i p_i g_i into differences, which do not cancel.)  A slot of
 // weight zero takes no part; every other expert's gradient is zero and is written.
-template <typename L, int NV, bool SOFTMAX>
+// One warp per token: the row without the choice is written whole (zeros; DENSE, for softmax as it is,
+// -p_e sum), then lane j its expert's value over it.
+template <int NV>
+__device__ __forceinline__ void store_some(float* p, int n, bool wide, const float (&v)[NV])
+{
+    if (NV % 4 == 0 && wide) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4)
+            if (i < n)
+                *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[(i + 1) % NV], v[(i + 2) % NV], v[(i + 3) % NV]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i < n) p[i] = v[i];
+    }
+}
+template <int NV>
+__device__ __forceinline__ void store_some(uint16_t* p, int n, bool wide, const float (&v)[NV])
+{
+    if (NV % 8 == 0 && wide) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 8)
+            if (i < n)
+                *reinterpret_cast<uint4*>(p + i) =
+                    make_uint4(bf16_rn(v[i]) | (bf16_rn(v[(i + 1) % NV]) << 16), bf16_rn(v[(i + 2) % NV]) | (bf16_rn(v[(i + 3) % NV]) << 16),
+                               bf16_rn(v[(i + 4) % NV]) | (bf16_rn(v[(i + 5) % NV]) << 16), bf16_rn(v[(i + 6) % NV]) | (bf16_rn(v[(i + 7) % NV]) << 16));
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i < n) store_logit(p + i, v[i]);
+    }
+}
+
+template <typename L, int NV, bool DENSE>
 __global__ void __launch_bounds__(128) moe_route_backward_kernel(const float* __restrict__ dw,
                                                                  const float* __restrict__ w,
                                                                  const int32_t* __restrict__ idx,
                                                                  const L* __restrict__ logits, int64_t T, int E,
-                                                                 int k, int renorm, float scale,
-                                                                 L* __restrict__ dlogits)
+                                                                 int k, bool wide, int sigmoid, int renorm,
+                                                                 float scale, L* dlogits)
 {
     griddep_launch_dependents();
     griddep_wait();
@@ -501,6 +648,27 @@ __global__ void __launch_bounds__(128) moe_route_backward_kernel(const float* __
             e = -1;
         }
     }
+    float x = 0.0f;
+    if ((DENSE || sigmoid) && e >= 0) x = load_logit(row + e);
+    float v[NV];
+    float top = -CUDART_INF_F, inv = 0.0f;
+    if (DENSE) {
+        load_some<NV>(row + lane * NV, E - lane * NV, wide, v);
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!(v[i] < CUDART_INF_F)) v[i] = -CUDART_INF_F;
+            top = fmaxf(top, v[i]);
+        }
+        top = warp_max(top);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            v[i] = v[i] > -CUDART_INF_F ? expf(v[i] - top) : 0.0f;
+            total += v[i];
+        }
+        total = warp_sum(total);
+        inv = total > 0.0f ? 1.0f / total : 0.0f;
+    }
     const bool live = e >= 0 && wt != 0.0f;
     const float p = live ? wt / scale : 0.0f;
     if (!live) g = 0.0f;
@@ -510,46 +678,20 @@ __global__ void __launch_bounds__(128) moe_route_backward_kernel(const float* __
     } else {
         d = g;
     }
-    if (!SOFTMAX && live) {
-        const float x = load_logit(row + e);
-        d *= 1.0f / (1.0f + expf(x));   // 1 - sigmoid(x)
-    }
+    if (sigmoid && live) d *= 1.0f / (1.0f + expf(x));   // 1 - sigmoid(x)
     d = live ? d * wt : 0.0f;
-
-    float sum = 0.0f, top = -CUDART_INF_F, inv = 0.0f;
-    float l[NV];
-    const bool dense = SOFTMAX && !renorm;
-    if (dense) {
-        sum = warp_sum(d);
-        float total = 0.0f;
+    const float sum = DENSE ? warp_sum(d) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = lane + 32 * i;
-            l[i] = -CUDART_INF_F;
-            if (c < E) {
-                const float x = load_logit(row + c);
-                if (x < CUDART_INF_F) l[i] = x;
-            }
-            top = fmaxf(top, l[i]);
-        }
-        top = warp_max(top);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) total += l[i] > -CUDART_INF_F ? expf(l[i] - top) : 0.0f;
-        total = warp_sum(total);
-        inv = total > 0.0f ? 1.0f / total : 0.0f;
+    for (int i = 0; i < NV; ++i) v[i] = DENSE ? -sum * (v[i] * inv) : 0.0f;
+    store_some<NV>(dlogits + t * E + lane * NV, E - lane * NV, wide, v);
+    // The same expert twice: each of its lanes writes the sum.
+    float mine = DENSE && x < CUDART_INF_F && x > -CUDART_INF_F ? -sum * (expf(x - top) * inv) : 0.0f;
+    for (int i = 0; i < k; ++i) {
+        const float di = __shfl_sync(kFull, d, i);
+        if (__shfl_sync(kFull, e, i) == e) mine += di;
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = lane + 32 * i;
-        float v = 0.0f;
-        if (dense && l[i] > -CUDART_INF_F) v = -sum * (expf(l[i] - top) * inv);
-        for (int j = 0; j < k; ++j) {
-            const int ej = __shfl_sync(kFull, e, j);
-            const float dj = __shfl_sync(kFull, d, j);
-            if (ej == c) v += dj;
-        }
-        if (c < E) store_logit(dlogits + t * E + c, v);
-    }
+    __syncwarp();   // behind the row's stores by other lanes
+    if (e >= 0) store_logit(dlogits + t * E + e, mine);
 }
 
 // ------------------------------------------------------------------------------------------

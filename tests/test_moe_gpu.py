@@ -99,6 +99,46 @@ def test_route_orders_keys_that_fp32_cannot_tell_apart():
         check_route(logits[t:t + 1], torch.float32, 12, bias, n_group=16, topk_group=9)
 
 
+@pytest.mark.parametrize("E", [24, 64, 96, 256, 288, 1024])
+@pytest.mark.parametrize("unit", [2.0 ** -22, -2.0 ** -22, 2.0 ** -149])
+def test_route_orders_logits_one_step_apart(E, unit):
+    # Neighbouring fp32 numbers around +-3, and the smallest there are: with and without groups, whole in a
+    # warp's lanes or not, and with a bias that leaves the order to binary64.
+    rng = np.random.default_rng(E)
+    start = 0.0 if unit == 2.0 ** -149 else 3.0 * np.sign(unit)
+    logits = np.stack([start + rng.permutation(E) * unit for _ in range(40)]).astype(np.float32)
+    for score in ("sigmoid", "softmax"):
+        for n_group, topk_group in ((1, 1), (8, 3), (3, 2) if E % 3 == 0 else (4, 3), (2, 1)):
+            check_route(logits, torch.float32, 8, score=score, n_group=n_group, topk_group=topk_group)
+            if unit != 2.0 ** -149:      # (sums that binary64 tells apart)
+                bias = np.full(E, -0.7, np.float32)
+                check_route(logits, torch.float32, 8, bias, score=score, n_group=n_group, topk_group=topk_group)
+
+
+@pytest.mark.parametrize("E,n_group,topk_group", [(256, 8, 4), (256, 16, 5), (128, 4, 2), (384, 12, 4), (512, 8, 8)])
+def test_route_many_tokens(E, n_group, topk_group):
+    # Enough tokens for every kind of near tie.
+    rng = np.random.default_rng(E + n_group)
+    for dtype in (torch.float32, torch.bfloat16):
+        logits = rng.normal(size=(3000, E))
+        for bias in (None, np.zeros(E), 0.05 * rng.normal(size=E)):
+            for score in ("sigmoid", "softmax"):
+                t = torch.from_numpy(logits.astype(np.float32)).to(dtype).cuda()
+                b = None if bias is None else f32_dev(bias)
+                idx, _ = ops.moe_route(t, 8, bias=b, score=score, n_group=n_group, topk_group=topk_group)
+                ok()
+                # The definition in torch's binary64, with sorts that keep the order of equals.
+                l = t.double()
+                key = l if bias is None else (torch.sigmoid(l) if score == "sigmoid" else torch.softmax(l, -1)) + b.double()
+                per = key.view(-1, n_group, E // n_group)
+                best = per.amax(-1) if bias is None else per.topk(2, -1).values.sum(-1)
+                kept = torch.sort(best, dim=-1, descending=True, stable=True).indices[:, :topk_group]
+                allowed = torch.zeros_like(best, dtype=torch.bool).scatter_(1, kept, True)
+                key = per.masked_fill(~allowed[:, :, None], -INF).view(-1, E)
+                want = torch.sort(key, dim=-1, descending=True, stable=True).indices[:, :8]
+                assert torch.equal(idx.long(), want)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_route_ties_go_to_the_lower_index(dtype):
     T, E = 5, 96
