@@ -157,8 +157,9 @@ __device__ __forceinline__ T warp_sum(T v)
 // expert (logit or bias -inf, NaN or +inf) has the key -inf.
 //
 // Keys are first formed in binary32 and truncated, with an error that is bounded below.  Where two
-// neighbours in the order found that way (or the groups on the two sides of the border) are nearer than
-// the bound, the token is done again with whole keys, in binary64 where there is a bias; that is rare.
+// neighbours in the order found that way are nearer than the bound, the candidates are put in order by
+// whole keys, in binary64 where there is a bias; where two groups at the border are, the token is done
+// again with whole keys throughout.  Both are rare.
 // MEASURED
 // Bound by latency and instruction issue; the logits are 8 MB.
 // ------------------------------------------------------------------------------------------
@@ -274,8 +275,10 @@ __device__ __forceinline__ int choose(const F (&key)[NV], const RouteShape& sh, 
 
 // The same choice from truncated keys, in about a third of the instructions: the low bits of a key's rank
 // hold its place in the lane (the lowest index the highest), so a lane's keys sort as plain integers
-// and the winner carries its index.  Ties of truncated keys go to the lower index; the border conditions
-// below make sure that the order found is that of the keys before truncation, or set *unsure.
+// and the winner carries its index.  Ties of truncated keys go to the lower index.  Where two neighbours in
+// this order are not more than `near` apart, the k and all that are within `near` of the k-th are put in
+// order by their whole keys, one a lane.  *unsure is set where that is not enough: two groups at the
+// border within near_group of each other, or more than 32 candidates.
 // Batcher's odd-even merge sort, descending.
 template <int N>
 __device__ __forceinline__ void sort_down(uint32_t (&r)[N])
@@ -301,9 +304,11 @@ __device__ __forceinline__ float key_of(uint32_t rank)   // of a rank above 1
 }
 
 // exact: truncation loses nothing (bf16 logits without a bias), so that ties are ties.
-template <int NV, typename Same>
+// same(p, q): experts p and q have the same logit and bias.  exactly(e): the whole key of expert e, asked
+// by the whole warp.
+template <int NV, typename Same, typename Exactly>
 __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteShape& sh, bool pair, bool exact,
-                                           float near, float near_group, Same same, bool* unsure)
+                                           float near, float near_group, Same same, Exactly exactly, bool* unsure)
 {
     constexpr uint32_t kPlace = NV - 1;   // NV is a power of two
     const int lane = threadIdx.x & 31, e0 = lane * NV;
@@ -372,23 +377,28 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
 #pragma unroll
         for (int i = 1; i < NV; ++i) head = max(head, rank[i]);
     }
-    int chosen = 0, last_e = 0;
-    float last = CUDART_INF_F;
-    const int rounds = !exact && sh.topk_group * per > sh.k ? sh.k + 1 : sh.k;
-    for (int j = 0; j < rounds; ++j) {
+    // The k best one after another, and then all that are too near the k-th to be left out for certain.
+    int chosen = 0, last_e = 0, n = 0;
+    float last = CUDART_INF_F, kth = CUDART_INF_F;
+    bool doubt = false;
+    const int limit = min(32, sh.topk_group * per);
+    for (; n < limit; ++n) {
+        if (exact && n == sh.k) break;
         const uint32_t top = __reduce_max_sync(kFull, head & ~kPlace);
+        const float value = value_of(top);
+        if (n >= sh.k) {
+            if (value == -CUDART_INF_F || kth - value > near) break;
+            doubt = true;
+        }
         const int who = __ffs(__ballot_sync(kFull, (head & ~kPlace) == top)) - 1;   // the lowest lane: the lowest index
         const int e = __shfl_sync(kFull, e0 + (int)(kPlace - (head & kPlace)), who);
-        if (!exact) {
-            const float value = value_of(top);
-            if (j > 0 && value > -CUDART_INF_F && !(last - value > near)) {
-                // Equal inputs have equal keys; at the border an equal neighbour may hide the next one.
-                if (j == sh.k || !same(last_e, e)) *unsure = true;
-            }
+        if (!exact) {   // equal inputs have equal keys
+            if (n < sh.k && value > -CUDART_INF_F && !(last - value > near) && !same(last_e, e)) doubt = true;
+            if (n == sh.k - 1) kth = value;
             last = value;
             last_e = e;
         }
-        if (lane == j) chosen = e;   // (round k is for the check only)
+        if (lane == n) chosen = e;
         if (NV <= 8) {
             if (lane == who) {
 #pragma unroll
@@ -405,6 +415,23 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
             }
             head = best;
         }
+    }
+    if (doubt) {
+        if (n == 32 && limit < sh.topk_group * per) *unsure = true;   // perhaps not all of them
+        // Lane i: candidate i's whole key, and how many come before it.
+        const double whole_key = exactly(chosen);
+        int before = 0;
+        for (int i = 0; i < n; ++i) {
+            const double other = __shfl_sync(kFull, whole_key, i);
+            const int other_e = __shfl_sync(kFull, chosen, i);
+            if (other > whole_key || (other == whole_key && other_e < chosen)) ++before;
+        }
+        int ordered = 0;
+        for (int j = 0; j < sh.k; ++j) {
+            const int e = __shfl_sync(kFull, chosen, __ffs(__ballot_sync(kFull, lane < n && before == j)) - 1);
+            if (lane == j) ordered = e;
+        }
+        chosen = ordered;
     }
     return chosen;
 }
@@ -552,9 +579,24 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ lo
         near = (bias ? (SOFTMAX ? 0x1p-16f : 0x1p-20f) + 0x1p-22f * largest : 0.0f) + 2.0f * kCut * largest + 4 * NV * 0x1p-149f;
     }
     bool unsure = false;
-    int chosen = choose_fast<NV>(key, sh, bias != nullptr, exact, near, 4.0f * near,
-                                 [&](int p, int q) { return load_logit(row + p) == load_logit(row + q) && (!bias || bias[p] == bias[q]); },
-                                 &unsure);
+    const auto same = [&](int p, int q) {
+        return load_logit(row + p) == load_logit(row + q) && (!bias || bias[p] == bias[q]);
+    };
+    const auto exactly = [&](int e) {
+        const double x = load_logit(row + e);
+        if (!bias) return x < CUDART_INF ? x : -CUDART_INF;
+        double sum = 0.0;
+        if (SOFTMAX) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (r.l[i] > -CUDART_INF_F) sum += exp((double)r.l[i] - (double)r.top);
+            sum = warp_sum(sum);
+        }
+        const double b = bias[e];
+        if (!(x > -CUDART_INF && x < CUDART_INF && b > -CUDART_INF && b < CUDART_INF)) return -CUDART_INF;
+        return (SOFTMAX ? exp(x - (double)r.top) / sum : 1.0 / (1.0 + exp(-x))) + b;
+    };
+    int chosen = choose_fast<NV>(key, sh, bias != nullptr, exact, near, 4.0f * near, same, exactly, &unsure);
     if (unsure) chosen = choose_exactly<L, NV, SOFTMAX>(row, bias, sh, wide);   // the same for the whole warp
 
     // Weights.  The renormalised ones divide scores by their sum, so scores that would underflow are
