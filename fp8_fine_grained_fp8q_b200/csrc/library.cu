@@ -74,17 +74,25 @@ bool allow_smem(Kernel kern, int bytes, std::atomic<bool> (&ready)[kMaxDevices])
     return true;
 }
 
+// s where n = 2^s nv, -1 where there is none.
+int lane_shift(int n, int nv)
+{
+    for (int s = 0; s < 6; ++s)
+        if (n == nv << s) return s;
+    return -1;
+}
+
 template <typename L, bool SOFTMAX>
 int launch_route(const void* logits, const float* bias, int64_t T, int E, int k, int n_group, int topk_group,
                  int renorm, float scale, int32_t* idx, float* w, cudaStream_t st)
 {
     const dim3 grid((unsigned)((T + 3) / 4));
     const L* l = static_cast<const L*>(logits);
-    const RouteShape sh{E, k, n_group, topk_group};
+    const int per = E / n_group;
     const bool wide = E % 8 == 0 && aligned16(logits) && aligned16(bias);
 #define FP8Q_ROUTE(NV)                                                                                             \
-    return launch_kernel(moe_route_kernel<L, NV, SOFTMAX>, grid, dim3(128), 0, st, false, l, bias, T, sh, wide, renorm, \
-                         scale, idx, w)
+    return launch_kernel(moe_route_kernel<L, NV, SOFTMAX>, grid, dim3(128), 0, st, false, l, bias, T,              \
+                         RouteShape{E, k, n_group, topk_group, per, lane_shift(per, NV)}, wide, renorm, scale, idx, w)
     if (E <= 32) FP8Q_ROUTE(1);
     if (E <= 64) FP8Q_ROUTE(2);
     if (E <= 128) FP8Q_ROUTE(4);

@@ -195,6 +195,8 @@ __device__ __forceinline__ void merge_two(F& a, F& b, F c, F d)
 
 struct RouteShape {
     int E, k, n_group, topk_group;
+    int per;     // experts of a group
+    int shift;   // a group is 2^shift whole lanes; -1: it is not
 };
 
 // Lane j: the j-th expert by key[i] (of expert lane * NV + i; -inf: masked).  `pair`: a group's score is
@@ -203,19 +205,18 @@ template <typename F, int NV>
 __device__ __forceinline__ int choose(const F (&key)[NV], const RouteShape& sh, bool pair)
 {
     typedef typename Rank<F>::type R;
-    const int lane = threadIdx.x & 31, e0 = lane * NV;
-    const int per = sh.E / sh.n_group;
+    const int lane = threadIdx.x & 31, e0 = lane * NV, per = sh.per;
     uint32_t allowed = kFull;   // bit g: experts of group g may be chosen
     if (sh.n_group > sh.topk_group) {
         F mine = lowest<F>();   // lane g: the score of group g
-        const int seg = per / NV;
-        if (seg * NV == per && (seg & (seg - 1)) == 0) {
+        if (sh.shift >= 0) {
             // A group is a power of two of whole lanes: the two largest by a butterfly in each.
             F a = lowest<F>(), b = lowest<F>();
 #pragma unroll
             for (int i = 0; i < NV; ++i) merge_two(a, b, key[i], lowest<F>());
-            for (int o = 1; o < seg; o <<= 1) merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
-            mine = __shfl_sync(kFull, pair && b > lowest<F>() ? a + b : a, (lane * seg) & 31);
+            for (int o = 1; o >> sh.shift == 0; o <<= 1)
+                merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
+            mine = __shfl_sync(kFull, pair && b > lowest<F>() ? a + b : a, (lane << sh.shift) & 31);
         } else {
             for (int g = 0; g < sh.n_group; ++g) {
                 F a = lowest<F>(), b = lowest<F>();
@@ -311,8 +312,7 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
                                            float near, float near_group, Same same, Exactly exactly, bool* unsure)
 {
     constexpr uint32_t kPlace = NV - 1;   // NV is a power of two
-    const int lane = threadIdx.x & 31, e0 = lane * NV;
-    const int per = sh.E / sh.n_group;
+    const int lane = threadIdx.x & 31, e0 = lane * NV, per = sh.per;
     // Masked: the lowest ranks there are, in the order of the index; an expert that is not there: 0.
     uint32_t rank[NV];
 #pragma unroll
@@ -322,8 +322,7 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
     }
     const auto value_of = [](uint32_t r) { return r >= 2u * NV ? key_of(r & ~kPlace) : -CUDART_INF_F; };
 
-    const int seg = per / NV;
-    const bool whole = seg * NV == per && (seg & (seg - 1)) == 0;   // a group is a power of two of whole lanes
+    const bool whole = sh.shift >= 0;
     const bool grouped = sh.n_group > sh.topk_group;
     // Up to eight keys are sorted; longer lists cost more to sort than to search.
     if (NV <= 8 && (whole || !grouped)) sort_down<NV>(rank);
@@ -338,8 +337,9 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
 #pragma unroll
                 for (int i = 0; i < NV; ++i) merge_two(a, b, key[i], -CUDART_INF_F);
             }
-            for (int o = 1; o < seg; o <<= 1) merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
-            mine = __shfl_sync(kFull, pair && b > -CUDART_INF_F ? a + b : a, (lane * seg) & 31);
+            for (int o = 1; o >> sh.shift == 0; o <<= 1)
+                merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
+            mine = __shfl_sync(kFull, pair && b > -CUDART_INF_F ? a + b : a, (lane << sh.shift) & 31);
         } else {
             for (int g = 0; g < sh.n_group; ++g) {
                 float a = -CUDART_INF_F, b = -CUDART_INF_F;
@@ -352,23 +352,38 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
                 if (lane == g) mine = pair && b > -CUDART_INF_F ? a + b : a;
             }
         }
-        int place = 0;
-        for (int g = 0; g < sh.n_group; ++g) {
-            const float other = __shfl_sync(kFull, mine, g);
-            if (other > mine || (other == mine && g < lane)) ++place;
+        // The best groups one after another, and the first that is left out.
+        uint32_t allowed = 0u, standing = lane < sh.n_group ? rank_of(mine) : 0u;
+        float in = 0.0f;
+        for (int j = 0; j <= sh.topk_group; ++j) {
+            const uint32_t top = __reduce_max_sync(kFull, standing);
+            const int g = __ffs(__ballot_sync(kFull, standing == top)) - 1;
+            const float score = key_of(top);
+            if (j == sh.topk_group) {
+                if (!exact && score > -CUDART_INF_F && !(in - score > near_group)) *unsure = true;
+            } else {
+                allowed |= 1u << g;
+                in = score;
+                if (lane == g) standing = 0u;
+            }
         }
-        if (lane >= sh.n_group) place = 32;
-        const uint32_t allowed = __ballot_sync(kFull, place < sh.topk_group);
-        if (!exact) {
-            const float in = __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, place == sh.topk_group - 1)) - 1);
-            const float out = __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, place == sh.topk_group)) - 1);
-            if (out > -CUDART_INF_F && !(in - out > near_group)) *unsure = true;
-        }
-        // Experts of the other groups are out.  (rank holds its place, so it may be sorted already.)
+        // Experts of the other groups are out.  (A rank holds its place, wherever sorting took it.)
+        if (whole) {
+            if (!((allowed >> (lane >> sh.shift)) & 1u)) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int g = whole ? lane / seg : (e0 + (int)(kPlace - (rank[i] & kPlace))) / per;
-            if (!((allowed >> (g & 31)) & 1u)) rank[i] = 0u;
+                for (int i = 0; i < NV; ++i) rank[i] = 0u;
+            }
+        } else {
+            int g = e0 / per, left = per - (e0 - g * per);   // rank is not sorted yet
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (left == 0) {
+                    left = per;
+                    ++g;
+                }
+                --left;
+                if (!((allowed >> (g & 31)) & 1u)) rank[i] = 0u;
+            }
         }
         if (NV <= 8 && !whole) sort_down<NV>(rank);
     }
@@ -610,12 +625,14 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ lo
     }
     const float best = warp_max(usable ? x : -CUDART_INF_F);
     float s = 0.0f;
-    if (usable) {
-        const float m = renorm ? (SOFTMAX ? best : fminf(best, 0.0f)) : 0.0f;
-        if (SOFTMAX)
-            s = renorm ? expf(x - m) : expf(x - r.top) / total;
-        else
-            s = x > 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - m) / (1.0f + expf(x));
+    if (SOFTMAX) {
+        if (usable) s = renorm ? expf(x - best) : expf(x - r.top) / total;
+    } else {
+        const float m = renorm ? fminf(best, 0.0f) : 0.0f;   // the same for the whole warp
+        const float z = expf(-fabsf(x));
+        float num = x > 0.0f ? 1.0f : z;
+        if (m < 0.0f) num = expf(x - m);
+        if (usable) s = num / (1.0f + z);
     }
     if (renorm) {
         const float sum = warp_sum(s);
