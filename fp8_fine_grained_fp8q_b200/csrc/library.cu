@@ -57,6 +57,8 @@ int launch_cluster(void (*kern)(KArgs...), int ctas, dim3 block, size_t smem, cu
     return launch_status();
 }
 
+// One CTA does this many slots as fast as a cluster starts and meets: 8 slots 3.1 us against 4.5, 1024
+// slots 4.8 against 5.1, 4096 slots 8.8 against 6.3.
 constexpr int64_t kPlanOneCta = 1024;
 
 // Lets a kernel have up to `bytes` of dynamic shared memory, once a device (`ready`: the kernel's own).
@@ -189,7 +191,6 @@ int fp8q_moe_plan(const int32_t* idx, int64_t T, int32_t k, int32_t E, int32_t* 
         const size_t bytes = (size_t)(E + 1) * sizeof(int32_t);
         return cudaMemsetAsync(offsets, 0, bytes, st) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
     }
-    // One CTA does a few thousand slots faster than a cluster starts and meets.
     const int ctas = T * k <= kPlanOneCta ? 1 : kPlanCtas;
     const auto plan = ctas == 1 ? moe_plan_kernel<1> : moe_plan_kernel<kPlanCtas>;
     static std::atomic<bool> ready[2][kMaxDevices];
@@ -236,8 +237,10 @@ int fp8q_moe_combine(const uint16_t* y, const int32_t* rows, const float* weight
     if (!y || !rows || !out) return FP8Q_ERR_ARG;
     if (!aligned16(y) || !aligned16(add) || !aligned16(out) || !aligned4(rows) || !aligned4(weights))
         return FP8Q_ERR_ALIGN;
-    return launch_kernel(moe_combine_kernel, dim3(grid_for((T * (C / 8) + 255) / 256, 8)), dim3(256), 0,
-                         (cudaStream_t)stream, false, y, rows, weights, add, T, (int)k, C, out);
+    const int64_t items = T * ((C / 8 + kCombineThreads - 1) / kCombineThreads);
+    if (items > kI32) return FP8Q_ERR_UNSUPPORTED;
+    return launch_kernel(moe_combine_kernel, dim3(grid_for(items, 8)), dim3(kCombineThreads), 0, (cudaStream_t)stream, false,
+                         y, rows, weights, add, (uint32_t)T, (uint32_t)k, (uint32_t)C, out);
 }
 
 int fp8q_moe_combine_dweight(const uint16_t* dout, const uint16_t* y, const int32_t* rows, int64_t T, int32_t k,

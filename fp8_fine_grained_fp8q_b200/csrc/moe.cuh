@@ -159,9 +159,9 @@ __device__ __forceinline__ T warp_sum(T v)
 // Keys are first formed in binary32 and truncated, with an error that is bounded below.  Where two
 // neighbours in the order found that way are nearer than the bound, the candidates are put in order by
 // whole keys, in binary64 where there is a bias; where two groups at the border are, the token is done
-// again with whole keys throughout.  Both are rare.
-// MEASURED
-// Bound by latency and instruction issue; the logits are 8 MB.
+// again with whole keys throughout.  Both are rare (binary64 for every token: 65 us instead of 16 below).
+// Bound by latency and instruction issue: 8192 tokens of 256 experts in 8 groups with a bias take 16 us,
+// without groups and bias 10 us (their 8 MB of logits 1.3 us); one token 3.7 us.
 // ------------------------------------------------------------------------------------------
 // Keys as unsigned integers of the same order, above 1.  0: not to be chosen (again); 1: masked.
 __device__ __forceinline__ uint32_t rank_of(float f)
@@ -274,12 +274,6 @@ __device__ __forceinline__ int choose(const F (&key)[NV], const RouteShape& sh, 
     return chosen;
 }
 
-// The same choice from truncated keys, in about a third of the instructions: the low bits of a key's rank
-// hold its place in the lane (the lowest index the highest), so a lane's keys sort as plain integers
-// and the winner carries its index.  Ties of truncated keys go to the lower index.  Where two neighbours in
-// this order are not more than `near` apart, the k and all that are within `near` of the k-th are put in
-// order by their whole keys, one a lane.  *unsure is set where that is not enough: two groups at the
-// border within near_group of each other, or more than 32 candidates.
 // Batcher's odd-even merge sort, descending.
 template <int N>
 __device__ __forceinline__ void sort_down(uint32_t (&r)[N])
@@ -304,6 +298,12 @@ __device__ __forceinline__ float key_of(uint32_t rank)   // of a rank above 1
     return __uint_as_float(rank ^ ((rank >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// The same choice from truncated keys, in about half the instructions: the low bits of a key's rank
+// hold its place in the lane (the lowest index the highest), so a lane's keys sort as plain integers
+// and the winner carries its index.  Ties of truncated keys go to the lower index.  Where two neighbours in
+// this order are not more than `near` apart, the k and all that are within `near` of the k-th are put in
+// order by their whole keys, one a lane.  *unsure is set where that is not enough: two groups at the
+// border within near_group of each other, or more than 32 candidates.
 // exact: truncation loses nothing (bf16 logits without a bias), so that ties are ties.
 // same(p, q): experts p and q have the same logit and bias.  exactly(e): the whole key of expert e, asked
 // by the whole warp.
@@ -756,11 +756,10 @@ __global__ void __launch_bounds__(128) moe_route_backward_kernel(const float* __
 // ------------------------------------------------------------------------------------------
 // The plan: a stable counting sort of the M = T k slots by expert, in one launch of one cluster.  Warp w
 // of CTA c owns a contiguous run of slots; it counts its experts 32 at a time, a slot's rank among the
-// 32 coming from one ballot per bit of the expert (match.any, which loops over the distinct values, took
-// three times as long).  The counts become starting rows by a scan over (expert, CTA, warp) through
+// 32 coming from one ballot per bit of the expert (with match.any, which loops over the distinct values,
+// 65536 slots took 22 us instead of 15).  The counts become starting rows by a scan over (expert, CTA, warp) through
 // distributed shared memory, and a second walk over the same slots places them.  No atomics on the rows,
-// so the order is a function of the input alone.  Bound by latency: one CTA alone took 135 us for
-// 65536 slots.
+// so the order is a function of the input alone.  Bound by latency: 65536 slots of 256 experts take 15 us.
 // ------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
@@ -1013,8 +1012,10 @@ __device__ __forceinline__ void group_rows(const GroupTable& t, int E, int g, in
 
 // ------------------------------------------------------------------------------------------
 // Dispatch, 1x128 codes: row rows[t,j] holds (weight of the slot) * x[t].  A warp takes four 128-element
-// tiles of one token (eight lanes each), reads them once and writes them to the token's k rows: bound
-// by the writes.  Without weights the k rows hold the same codes, which are formed once.
+// tiles of one token (eight lanes each), reads them once and writes them to the token's k rows.  Without
+// weights the k rows hold the same codes, which are formed once.
+// Bound by the writes: 8192 tokens x 8 of 7168 channels take 130 us (4.6 TB/s), 100 without the scales,
+// whose neighbours in memory belong to other tokens and so leave 4 bytes at a time.
 // ------------------------------------------------------------------------------------------
 template <bool WEIGHTED>
 __global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* __restrict__ x,
@@ -1114,9 +1115,10 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* 
 // previous tile is quantised.  Warp w quantises channels 16w .. 16w+15: lane (r, h) = (lane >> 1,
 // lane & 1) holds rows 8r .. 8r+7 of channels 8h .. 8h+7, so the column maxima need shuffles only, and a
 // channel's 128 codes leave as one line, 8 bytes from each r.  One barrier a tile.
-// Bound by the writes, with the arithmetic close behind.  Tiles are ordered by channel block first: at
-// any time the whole grid gathers from a few channel blocks of x (2 MB per 128 channels of 8192 tokens),
-// so a token's k reads find it in L2 although x as a whole need not fit.
+// Tiles are ordered by channel block first: at any time the whole grid gathers from a few channel blocks
+// of x (2 MB per 128 channels of 8192 tokens), so a token's k reads find it in L2 although x as a whole need
+// not fit.  65536 rows of 7168 channels in 645 groups take 207 us: the copies (through L2) and stores
+// alone 154 us, the arithmetic and stores alone 194 us.
 // ------------------------------------------------------------------------------------------
 // 16-byte piece c of row r of a staged tile (256 bytes a row) lies at piece c ^ 2 ((r >> 3) & 3) of the
 // row: the four r of a quarter-warp then read different banks.
@@ -1341,7 +1343,10 @@ __global__ void __launch_bounds__(256, 3) moe_dispatch_cols_kernel(
 
 // ------------------------------------------------------------------------------------------
 // Combine: out[t] = add[t] + sum_j w[t,j] y[rows[t,j]], summed in FP32 in the order of j and rounded
-// once.  A slot of weight zero is not read.  Each thread owns 8 channels of one token.
+// once.  A slot of weight zero is not read.  A CTA takes 1024 channels of one token, a thread 8 of them;
+// the loads of eight rows are in flight together.
+// Bound by HBM: 65536 rows of 7168 channels to 8192 tokens, with an addend, take 179 us, 6.55 TB/s (198 us
+// with one row's load after another).
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void fma8(float (&acc)[8], float w, const uint4& u)
 {
@@ -1353,37 +1358,50 @@ __device__ __forceinline__ void fma8(float (&acc)[8], float w, const uint4& u)
     }
 }
 
-__global__ void __launch_bounds__(256) moe_combine_kernel(const uint16_t* __restrict__ y,
-                                                          const int32_t* __restrict__ rows,
-                                                          const float* __restrict__ weights,
-                                                          const uint16_t* __restrict__ add, int64_t T, int k,
-                                                          int64_t C, uint16_t* __restrict__ out)
+constexpr int kCombineThreads = 128;
+
+__global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(
+    const uint16_t* __restrict__ y, const int32_t* __restrict__ rows, const float* __restrict__ weights,
+    const uint16_t* __restrict__ add, uint32_t T, uint32_t k, uint32_t C, uint16_t* __restrict__ out)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t units = C >> 3, M = T * k;
-    const int64_t n = T * units;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t t = i / units, u = i - t * units;
+    const uint32_t units = C >> 3, chunks = (units + kCombineThreads - 1) / kCombineThreads, items = T * chunks;
+    const int32_t M = (int32_t)(T * k);
+    for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const uint32_t t = it / chunks, u = (it - t * chunks) * kCombineThreads + threadIdx.x;
+        if (u >= units) continue;
         float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        for (int j = 0; j < k; ++j) {
-            const float w = weights ? __ldg(weights + t * k + j) : 1.0f;
-            const int32_t r = __ldg(rows + t * k + j);
-            if (w == 0.0f) continue;
-            if (r < 0 || r >= M) {
-                latch_status(kDevBadIndex);
-                continue;
+        for (uint32_t j0 = 0; j0 < k; j0 += 8) {
+            float w[8];
+            uint4 v[8];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                w[j] = 0.0f;
+                v[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (j0 + j < k) {
+                    w[j] = weights ? __ldg(weights + t * k + j0 + j) : 1.0f;
+                    const int32_t r = __ldg(rows + t * k + j0 + j);
+                    if (r < 0 || r >= M) {
+                        if (w[j] != 0.0f) latch_status(kDevBadIndex);
+                        w[j] = 0.0f;
+                    }
+                    if (w[j] != 0.0f) v[j] = __ldg(reinterpret_cast<const uint4*>(y + (size_t)r * C) + u);
+                }
             }
-            fma8(acc, w, __ldg(reinterpret_cast<const uint4*>(y + (int64_t)r * C) + u));
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)
+                if (w[j] != 0.0f) fma8(acc, w[j], v[j]);
         }
-        if (add) fma8(acc, 1.0f, __ldg(reinterpret_cast<const uint4*>(add + t * C) + u));
-        reinterpret_cast<uint4*>(out + t * C)[u] =
+        if (add) fma8(acc, 1.0f, __ldg(reinterpret_cast<const uint4*>(add + (size_t)t * C) + u));
+        reinterpret_cast<uint4*>(out + (size_t)t * C)[u] =
             make_uint4(bf16_rn(acc[0]) | (bf16_rn(acc[1]) << 16), bf16_rn(acc[2]) | (bf16_rn(acc[3]) << 16),
                        bf16_rn(acc[4]) | (bf16_rn(acc[5]) << 16), bf16_rn(acc[6]) | (bf16_rn(acc[7]) << 16));
     }
 }
 
-// dw[t,j] = <dout[t], y[rows[t,j]]>: one warp per slot, eight FP32 partial sums a lane.
+// dw[t,j] = <dout[t], y[rows[t,j]]>: one warp per slot, eight FP32 partial sums a lane.  Bound by HBM:
+// 65536 rows of 7168 channels take 168 us, 6.3 TB/s.
 __global__ void __launch_bounds__(256) moe_combine_dweight_kernel(const uint16_t* __restrict__ dout,
                                                                   const uint16_t* __restrict__ y,
                                                                   const int32_t* __restrict__ rows, int64_t T, int k,
@@ -1539,7 +1557,8 @@ __global__ void __launch_bounds__(256, 2) swiglu_quant_kernel(const uint16_t* __
 // 8w .. 8w+7, its lane r rows 4r .. 4r+3: the 96 values (three an element) are computed once and stay in
 // registers until both quantisations are done.  Columns lie inside a warp, so their scales need shuffles
 // only and their codes leave as whole lines; rows meet in shared memory.
-// The values fill the register file with one CTA an SM; bound by instruction issue, not far above HBM.
+// The values fill the register file with one CTA an SM.  Bound by instruction issue (0.58 of the slots)
+// and the latencies between three barriers: 65536 x 2048 in 645 groups take 309 us, 4.0 TB/s.
 // ------------------------------------------------------------------------------------------
 constexpr int kBackThreads = 512;
 constexpr int kBackStage = 128 * 256 + 2 * 128 * 128 + 2 * 128 * 4;   // da, the codes of g and u, their scales

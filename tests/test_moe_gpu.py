@@ -735,6 +735,25 @@ def test_first_use_inside_a_capture():
     assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
 
 
+def test_no_tokens_anywhere():
+    E, k, C, I = 6, 2, 256, 128
+    bf = lambda *shape: torch.empty(*shape, dtype=torch.bfloat16, device="cuda")   # noqa: E731
+    idx, w = ops.moe_route(torch.empty(0, E, device="cuda"), k)
+    plan = ops.moe_plan(idx, E)
+    q, s, qt, st = ops.moe_dispatch(bf(0, C), plan, weights=w, transposed=True)
+    y = bf(0, C)
+    out, dw = ops.moe_combine(y, plan, weights=w), ops.moe_combine_dweight(bf(0, C), y, plan)
+    d = ops.moe_route_backward(dw, w, idx, torch.empty(0, E, device="cuda"))
+    a = ops.swiglu_quant(bf(0, 2 * I))
+    g = ops.swiglu_backward_quant(bf(0, I), a[2], a[3], offsets=plan.offsets)
+    ops.swiglu_backward_quant(bf(0, I), a[2], a[3])
+    # The experts' weight gradients of no tokens are zero.
+    dw1 = ops.grouped_gemm_blockscaled_wgrad(g[2], g[3], qt, st, plan.offsets, 0)
+    ok()
+    assert not host(plan.offsets).any() and not host(dw1).any()
+    assert [tuple(t.shape) for t in (idx, q, out, dw, d, a[0])] == [(0, k), (0, C), (0, C), (0, k), (0, E), (0, I)]
+
+
 # -- sizes whose offsets pass 32 bits, against the library's own quantisers ------------------------------ #
 
 def test_dispatch_and_combine_past_32_bit_offsets():
