@@ -1125,7 +1125,12 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_kernel(const uint16_t* 
 __device__ __forceinline__ uint32_t stage_at(int r, int c) { return r * 256 + ((c ^ (((r >> 3) & 3) << 1)) << 4); }
 
 constexpr int kStageBytes = 128 * 256;
-constexpr int gather_smem(int E) { return 2 * kStageBytes + 3 * 1024 + group_table_bytes(E); }
+struct GatherSmem {   // byte offsets
+    static constexpr int token = 2 * kStageBytes;          // [3 items][128], -1: no row
+    static constexpr int weight = token + 3 * 128 * 4;     // [3 items][128]
+    static constexpr int table = weight + 3 * 128 * 4;
+};
+constexpr int gather_smem(int E) { return GatherSmem::table + group_table_bytes(E); }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live)   // zeros unless live
 {
@@ -1211,9 +1216,9 @@ __global__ void __launch_bounds__(256, 3) moe_dispatch_cols_kernel(
     griddep_launch_dependents();
     griddep_wait();
     extern __shared__ __align__(16) uint8_t smem[];
-    int* s_token = reinterpret_cast<int*>(smem + 2 * kStageBytes);               // [3][128], -1: no row
-    float* s_weight = reinterpret_cast<float*>(smem + 2 * kStageBytes + 1536);   // [3][128]
-    const GroupTable table(smem + 2 * kStageBytes + 3072, E);
+    int* s_token = reinterpret_cast<int*>(smem + GatherSmem::token);
+    float* s_weight = reinterpret_cast<float*>(smem + GatherSmem::weight);
+    const GroupTable table(smem + GatherSmem::table, E);
     if (!group_table(table, offsets, E, M, Kcap)) return;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, r = lane >> 1, h = lane & 1;
     const uint32_t stage = smem_u32(smem);
