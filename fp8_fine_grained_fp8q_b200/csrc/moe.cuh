@@ -8,6 +8,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ptx.cuh"
 #include "quant.cuh"
 
@@ -1559,11 +1561,12 @@ __global__ void __launch_bounds__(256, 2) swiglu_quant_kernel(const uint16_t* __
 // second GEMM's Wgrad operand), so a is never kept between the passes.
 // One CTA of 16 warps takes tiles of one padded group (128 rows) x 128 columns of I, whose inputs come
 // into shared memory by asynchronous copies while the tile before is worked on.  Warp w owns columns
-// 8w .. 8w+7, its lane r rows 4r .. 4r+3: the 96 values (three an element) are computed once and stay in
+// 8w .. 8w+7, its lane r rows 4r .. 4r+3 (2r, 2r+1 in a group of at most 64 rows: 2000 rows over 256 experts
+// take 86 us instead of 101): the 96 values, three an element, are computed once and stay in
 // registers until both quantisations are done.  Columns lie inside a warp, so their scales need shuffles
 // only and their codes leave as whole lines; rows meet in shared memory.
 // The values fill the register file with one CTA an SM.  Bound by instruction issue (0.58 of the slots)
-// and the latencies between three barriers: 65536 x 2048 in 645 groups take 309 us, 4.0 TB/s.
+// and the latencies between three barriers: 65536 x 2048 in 645 groups take 300 us, 4.1 TB/s.
 // ------------------------------------------------------------------------------------------
 constexpr int kBackThreads = 512;
 constexpr int kBackStage = 128 * 256 + 2 * 128 * 128 + 2 * 128 * 4;   // da, the codes of g and u, their scales
@@ -1582,7 +1585,7 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
 
-// The values of four E4M3 codes.
+// The values of four E4M3 codes; fp16 is widened by a mixed-precision x + (-0), as bf16 in widen().
 __device__ __forceinline__ void dec_e4m3x4(uint32_t w, float2 (&f)[2])
 {
     asm("{.reg .b16 c0, c1, l, h;\n\t"
@@ -1590,14 +1593,14 @@ __device__ __forceinline__ void dec_e4m3x4(uint32_t w, float2 (&f)[2])
         "mov.b32 {c0, c1}, %4;\n\t"
         "cvt.rn.f16x2.e4m3x2 p, c0;\n\t"
         "mov.b32 {l, h}, p;\n\t"
-        "cvt.f32.f16 %0, l;\n\t"
-        "cvt.f32.f16 %1, h;\n\t"
+        "add.f32.f16 %0, l, %5;\n\t"
+        "add.f32.f16 %1, h, %5;\n\t"
         "cvt.rn.f16x2.e4m3x2 p, c1;\n\t"
         "mov.b32 {l, h}, p;\n\t"
-        "cvt.f32.f16 %2, l;\n\t"
-        "cvt.f32.f16 %3, h;}"
+        "add.f32.f16 %2, l, %5;\n\t"
+        "add.f32.f16 %3, h, %5;}"
         : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y)
-        : "r"(w));
+        : "r"(w), "f"(-0.0f));
 }
 
 // max |.| over the warp's 32 lanes of eight values each: lane l ends with that of value l & 7.
@@ -1708,99 +1711,123 @@ __global__ void __launch_bounds__(kBackThreads, 1) swiglu_backward_kernel(
         if (tile != blockIdx.x) store_rows(place[(slot + 3) & 3]);   // the tile before's
 
         const uint8_t* in = smem + buf * kBackStage;
-        float2 dg[4][4], du[4][4], ac[4][4];   // [row][pair of columns]
-        float rg[4], ru[4];                    // row maxima of dg and du
+        const auto work = [&](auto rows_of_a_lane) {
+            constexpr int R = decltype(rows_of_a_lane)::value;
+            float2 dg[R][4], du[R][4], ac[R][4];   // [row][pair of columns]
+            float rg[R], ru[R];                    // row maxima of dg and du
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = 4 * lane + i;
-            const uint4 dw = *reinterpret_cast<const uint4*>(in + row * 256 + ((w ^ (lane & 7)) << 4));
-            const uint2 gc = *reinterpret_cast<const uint2*>(in + 32768 + row * 128 + (((w >> 1) ^ (lane & 7)) << 4) + 8 * (w & 1));
-            const uint2 uc = *reinterpret_cast<const uint2*>(in + 49152 + row * 128 + (((w >> 1) ^ (lane & 7)) << 4) + 8 * (w & 1));
-            const float gs = *reinterpret_cast<const float*>(in + 65536 + 4 * row);
-            const float us = *reinterpret_cast<const float*>(in + 65536 + 512 + 4 * row);
-            rg[i] = ru[i] = 0.0f;
-            float2 gf[4], uf[4];
-            dec_e4m3x4(gc.x, reinterpret_cast<float2 (&)[2]>(gf[0]));
-            dec_e4m3x4(gc.y, reinterpret_cast<float2 (&)[2]>(gf[2]));
-            dec_e4m3x4(uc.x, reinterpret_cast<float2 (&)[2]>(uf[0]));
-            dec_e4m3x4(uc.y, reinterpret_cast<float2 (&)[2]>(uf[2]));
+            for (int i = 0; i < R; ++i) {
+                const int row = R * lane + i, turn = (row >> 2) & 7;
+                const uint8_t* code = in + 32768 + row * 128 + (((w >> 1) ^ turn) << 4) + 8 * (w & 1);
+                const uint4 dw = *reinterpret_cast<const uint4*>(in + row * 256 + ((w ^ turn) << 4));
+                const uint2 gc = *reinterpret_cast<const uint2*>(code);
+                const uint2 uc = *reinterpret_cast<const uint2*>(code + 16384);
+                const float gs = *reinterpret_cast<const float*>(in + 65536 + 4 * row);
+                const float us = *reinterpret_cast<const float*>(in + 65536 + 512 + 4 * row);
+                rg[i] = ru[i] = 0.0f;
+                float2 gf[4], uf[4];
+                dec_e4m3x4(gc.x, reinterpret_cast<float2 (&)[2]>(gf[0]));
+                dec_e4m3x4(gc.y, reinterpret_cast<float2 (&)[2]>(gf[2]));
+                dec_e4m3x4(uc.x, reinterpret_cast<float2 (&)[2]>(uf[0]));
+                dec_e4m3x4(uc.y, reinterpret_cast<float2 (&)[2]>(uf[2]));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 d = widen(word(dw, j)), x = mul2(gf[j], both(gs)), u = mul2(uf[j], both(us));
-                const float2 r = sigmoid2(x), sx = mul2(x, r);
-                // r + sx (1 - r)
-                dg[i][j] = mul2(mul2(d, u), fma2(sx, fma2(r, both(-1.0f), both(1.0f)), r));
-                du[i][j] = mul2(d, sx);
-                ac[i][j] = mul2(u, sx);
-                rg[i] = max_abs(rg[i], dg[i][j].x, dg[i][j].y);
-                ru[i] = max_abs(ru[i], du[i][j].x, du[i][j].y);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 d = widen(word(dw, j)), x = mul2(gf[j], both(gs)), u = mul2(uf[j], both(us));
+                    const float2 r = sigmoid2(x), sx = mul2(x, r);
+                    // r + sx (1 - r)
+                    dg[i][j] = mul2(mul2(d, u), fma2(sx, fma2(r, both(-1.0f), both(1.0f)), r));
+                    du[i][j] = mul2(d, sx);
+                    ac[i][j] = mul2(u, sx);
+                    rg[i] = max_abs(rg[i], dg[i][j].x, dg[i][j].y);
+                    ru[i] = max_abs(ru[i], du[i][j].x, du[i][j].y);
+                }
             }
-        }
-        *reinterpret_cast<float4*>(red + w * 128 + 4 * lane) = make_float4(rg[0], rg[1], rg[2], rg[3]);
-        *reinterpret_cast<float4*>(red + 2048 + w * 128 + 4 * lane) = make_float4(ru[0], ru[1], ru[2], ru[3]);
-        __syncthreads();
-        if (tid < 256) {   // the row scales: thread (dg or du, row)
-            const int row = tid & 127;
-            const float* p = red + (tid >> 7) * 2048 + row;
-            float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) m = fmaxf(fmaxf(m, p[128 * i]), p[128 * i + 128]);
-            float sc, inv;
-            group_scale<false>(m, sc, inv);
-            inv_row[tid] = inv;
-            if (row < nvalid) s[(int64_t)((tid >> 7) * IB + ib) * M + r0 + row] = sc;
-        }
-        // Columns.  Lanes 8v + c: the scale of column c of value v (dg, du, a).
-        auto column_max = [&](const float2 (&x)[4][4]) {
-            float m[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                m[2 * j] = max_abs(max_abs(0.0f, x[0][j].x, x[1][j].x), x[2][j].x, x[3][j].x);
-                m[2 * j + 1] = max_abs(max_abs(0.0f, x[0][j].y, x[1][j].y), x[2][j].y, x[3][j].y);
+            for (int i = 0; i < R; i += 2) {
+                *reinterpret_cast<float2*>(red + w * 128 + R * lane + i) = make_float2(rg[i], rg[i + 1]);
+                *reinterpret_cast<float2*>(red + 2048 + w * 128 + R * lane + i) = make_float2(ru[i], ru[i + 1]);
             }
-            return max_of_eight(m, lane);
+            __syncthreads();
+            if (tid < 256) {   // the row scales: thread (dg or du, row); rows from nvalid on hold anything
+                const int row = tid & 127;
+                const float* p = red + (tid >> 7) * 2048 + row;
+                float m = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) m = fmaxf(fmaxf(m, p[128 * i]), p[128 * i + 128]);
+                float sc, inv;
+                group_scale<false>(m, sc, inv);
+                inv_row[tid] = inv;
+                if (row < nvalid) s[(int64_t)((tid >> 7) * IB + ib) * M + r0 + row] = sc;
+            }
+            // Columns.  Lanes 8v + c: the scale of column c of value v (dg, du, a).
+            auto column_max = [&](const float2 (&x)[R][4]) {
+                float m[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    m[2 * j] = m[2 * j + 1] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < R; i += 2) {
+                        m[2 * j] = max_abs(m[2 * j], x[i][j].x, x[i + 1][j].x);
+                        m[2 * j + 1] = max_abs(m[2 * j + 1], x[i][j].y, x[i + 1][j].y);
+                    }
+                }
+                return max_of_eight(m, lane);
+            };
+            {
+                const float m0 = column_max(dg), m1 = column_max(du), m2 = column_max(ac);
+                const int v = lane >> 3;
+                float sc, inv;
+                group_scale<false>(v == 0 ? m0 : v == 1 ? m1 : m2, sc, inv);
+                const uint32_t col = ib * 128 + 8 * w + (lane & 7);
+                if (v < 2) st[(int64_t)g * 2 * I + v * I + col] = sc;
+                if (v == 2) ast[(int64_t)g * I + col] = sc;
+                if (v < 3) inv_col[lane] = inv;
+            }
+            __syncwarp();
+            const int64_t corner = (int64_t)(ib * 128 + 8 * w) * Kcap + (int64_t)g * 128 + R * lane;
+            auto columns = [&](const float2 (&x)[R][4], const float* inv, uint8_t* out) {
+                const float4 i0 = *reinterpret_cast<const float4*>(inv), i1 = *reinterpret_cast<const float4*>(inv + 4);
+                const float2 f[4] = {{i0.x, i0.y}, {i0.z, i0.w}, {i1.x, i1.y}, {i1.z, i1.w}};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint8_t* even = out + (uint64_t)(2 * j) * (uint32_t)Kcap;
+                    uint8_t* odd = out + (uint64_t)(2 * j + 1) * (uint32_t)Kcap;
+                    const float2 a = mul2(x[0][j], f[j]), b = mul2(x[1][j], f[j]);
+                    if (R == 4) {
+                        const float2 c = mul2(x[R - 2][j], f[j]), d = mul2(x[R - 1][j], f[j]);
+                        *reinterpret_cast<uint32_t*>(even) = codes4(a.x, b.x, c.x, d.x);
+                        *reinterpret_cast<uint32_t*>(odd) = codes4(a.y, b.y, c.y, d.y);
+                    } else {   // rows 64 .. 127 are padding
+                        *reinterpret_cast<uint16_t*>(even) = (uint16_t)e4m3x2(a.x, b.x);
+                        *reinterpret_cast<uint16_t*>(odd) = (uint16_t)e4m3x2(a.y, b.y);
+                        *reinterpret_cast<uint16_t*>(even + 64) = 0;
+                        *reinterpret_cast<uint16_t*>(odd + 64) = 0;
+                    }
+                }
+            };
+            columns(ac, inv_col + 16, aqt + corner);
+            columns(dg, inv_col, qt + corner);
+            columns(du, inv_col + 8, qt + (int64_t)I * Kcap + corner);
+            __syncthreads();
+            // Rows: 8 bytes of a row from each warp, staged (8-byte unit w of row r at w ^ ((r >> 2) & 15)); they
+            // are written behind the next tile's first barrier.
+            auto stage_rows = [&](const float2 (&x)[R][4], const float* inv, uint8_t* to) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int row = R * lane + i;
+                    const float2 f = both(inv[row]);
+                    const float2 a = mul2(x[i][0], f), b = mul2(x[i][1], f), c = mul2(x[i][2], f), d = mul2(x[i][3], f);
+                    *reinterpret_cast<uint2*>(to + row * 128 + ((w ^ ((row >> 2) & 15)) << 3)) =
+                        make_uint2(codes4(a.x, a.y, b.x, b.y), codes4(c.x, c.y, d.x, d.y));
+                }
+            };
+            stage_rows(dg, inv_row, smem + BackSmem::codes);
+            stage_rows(du, inv_row + 128, smem + BackSmem::codes + 16384);
         };
-        {
-            const float m0 = column_max(dg), m1 = column_max(du), m2 = column_max(ac);
-            const int v = lane >> 3;
-            float sc, inv;
-            group_scale<false>(v == 0 ? m0 : v == 1 ? m1 : m2, sc, inv);
-            const uint32_t col = ib * 128 + 8 * w + (lane & 7);
-            if (v < 2) st[(int64_t)g * 2 * I + v * I + col] = sc;
-            if (v == 2) ast[(int64_t)g * I + col] = sc;
-            if (v < 3) inv_col[lane] = inv;
-        }
-        __syncwarp();
-        const int64_t corner = (int64_t)(ib * 128 + 8 * w) * Kcap + (int64_t)g * 128 + 4 * lane;
-        auto columns = [&](const float2 (&x)[4][4], const float* inv, uint8_t* out) {
-            const float4 i0 = *reinterpret_cast<const float4*>(inv), i1 = *reinterpret_cast<const float4*>(inv + 4);
-            const float2 f[4] = {{i0.x, i0.y}, {i0.z, i0.w}, {i1.x, i1.y}, {i1.z, i1.w}};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 a = mul2(x[0][j], f[j]), b = mul2(x[1][j], f[j]), c = mul2(x[2][j], f[j]), d = mul2(x[3][j], f[j]);
-                *reinterpret_cast<uint32_t*>(out + (uint64_t)(2 * j) * (uint32_t)Kcap) = codes4(a.x, b.x, c.x, d.x);
-                *reinterpret_cast<uint32_t*>(out + (uint64_t)(2 * j + 1) * (uint32_t)Kcap) = codes4(a.y, b.y, c.y, d.y);
-            }
-        };
-        columns(ac, inv_col + 16, aqt + corner);
-        columns(dg, inv_col, qt + corner);
-        columns(du, inv_col + 8, qt + (int64_t)I * Kcap + corner);
-        __syncthreads();
-        // Rows: 8 bytes of a row from each warp, staged (8-byte unit w of row r at w ^ ((r >> 2) & 15)); they
-        // are written behind the next tile's first barrier.
-        auto stage_rows = [&](const float2 (&x)[4][4], const float* inv, uint8_t* to) {
-            const float4 i4 = *reinterpret_cast<const float4*>(inv + 4 * lane);
-            const float f[4] = {i4.x, i4.y, i4.z, i4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 a = mul2(x[i][0], both(f[i])), b = mul2(x[i][1], both(f[i])), c = mul2(x[i][2], both(f[i])),
-                             d = mul2(x[i][3], both(f[i]));
-                *reinterpret_cast<uint2*>(to + (4 * lane + i) * 128 + ((w ^ (lane & 15)) << 3)) =
-                    make_uint2(codes4(a.x, a.y, b.x, b.y), codes4(c.x, c.y, d.x, d.y));
-            }
-        };
-        stage_rows(dg, inv_row, smem + BackSmem::codes);
-        stage_rows(du, inv_row + 128, smem + BackSmem::codes + 16384);
+        if (nvalid > 64)
+            work(std::integral_constant<int, 4>());
+        else
+            work(std::integral_constant<int, 2>());
     }
     __syncthreads();
     if (blockIdx.x < tiles) store_rows(place[(slot + 3) & 3]);

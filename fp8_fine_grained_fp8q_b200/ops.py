@@ -553,8 +553,8 @@ def moe_route_backward(dw: torch.Tensor, w: torch.Tensor, idx: torch.Tensor, log
         raise ValueError(f"dw, w and idx must have shape {(T, k)}, got {tuple(dw.shape)}, {tuple(w.shape)} and "
                          f"{tuple(idx.shape)}")
     out = _made(out, "out", logits.dtype, dev, T, E)
-    _launch("fp8q_moe_route_backward", dev, dw.data_ptr(), w.data_ptr(), idx.data_ptr(), logits.data_ptr(), kind, T, E, k, fn,
-            int(renormalize), scale, out.data_ptr())
+    _launch("fp8q_moe_route_backward", dev, dw.data_ptr(), w.data_ptr(), idx.data_ptr(), logits.data_ptr(), kind,
+            T, E, k, fn, int(renormalize), scale, out.data_ptr())
     return out
 
 
@@ -627,7 +627,8 @@ def moe_combine_dweight(dout: torch.Tensor, y: torch.Tensor, plan: MoePlan, out:
     if dout.shape[0] != T or tuple(y.shape) != (T * k, C):
         raise ValueError(f"dout must be [{T}, C] and y [{T * k}, C], got {tuple(dout.shape)} and {tuple(y.shape)}")
     out = _made(out, "out", torch.float32, dev, T, k)
-    _launch("fp8q_moe_combine_dweight", dev, dout.data_ptr(), y.data_ptr(), plan.rows.data_ptr(), T, k, C, out.data_ptr())
+    _launch("fp8q_moe_combine_dweight", dev, dout.data_ptr(), y.data_ptr(), plan.rows.data_ptr(), T, k, C,
+            out.data_ptr())
     return out
 
 
