@@ -50,6 +50,10 @@ int launch_cluster(void (*kern)(KArgs...), int ctas, dim3 block, size_t smem, cu
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return launch_status();
+    cudaGetLastError();
+    if (cfg.numAttrs == 1) return FP8Q_ERR_CUDA;
+    cfg.numAttrs = 1;   // the driver refused the combination: launch in plain stream order
     if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
         cudaGetLastError();
         return FP8Q_ERR_CUDA;
