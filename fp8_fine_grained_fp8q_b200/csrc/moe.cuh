@@ -5,6 +5,7 @@
 // one pass: quantised outputs leave from registers, gathers replace copies.
 #pragma once
 
+#include <float.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -300,6 +301,10 @@ __device__ __forceinline__ float key_of(uint32_t rank)   // of a rank above 1
     return __uint_as_float(rank ^ ((rank >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// A group's score from its two largest keys.  A sum that leaves fp32 stays finite: an infinite one would be a
+// masked group's.
+__device__ __forceinline__ float pair_score(float a, float b) { return fminf(fmaxf(a + b, -FLT_MAX), FLT_MAX); }
+
 // The same choice from truncated keys, in about half the instructions: the low bits of a key's rank
 // hold its place in the lane (the lowest index the highest), so a lane's keys sort as plain integers
 // and the winner carries its index.  Ties of truncated keys go to the lower index.  Where two neighbours in
@@ -341,7 +346,7 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
             }
             for (int o = 1; o >> sh.shift == 0; o <<= 1)
                 merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
-            mine = __shfl_sync(kFull, pair && b > -CUDART_INF_F ? a + b : a, (lane << sh.shift) & 31);
+            mine = __shfl_sync(kFull, pair && b > -CUDART_INF_F ? pair_score(a, b) : a, (lane << sh.shift) & 31);
         } else {
             for (int g = 0; g < sh.n_group; ++g) {
                 float a = -CUDART_INF_F, b = -CUDART_INF_F;
@@ -351,7 +356,7 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1)
                     merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
-                if (lane == g) mine = pair && b > -CUDART_INF_F ? a + b : a;
+                if (lane == g) mine = pair && b > -CUDART_INF_F ? pair_score(a, b) : a;
             }
         }
         // The best groups one after another, and the first that is left out.

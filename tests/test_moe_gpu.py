@@ -201,6 +201,39 @@ def test_route_bias_masks_too():
     assert bool(torch.isnan(w).all())
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E", [64, 96, 512])
+def test_route_masks_of_the_lowest_value(E, score):
+    # A mask of fp32's lowest finite number is a key like any other: below every ordinary one, above -inf.  The
+    # sum of two of them leaves fp32.
+    rng = np.random.default_rng(E)
+    low = float(torch.finfo(torch.float32).min)
+    per = E // 8
+    l = rng.normal(size=(40, E)).astype(np.float32)
+    masked = l.copy()
+    masked[:, rng.random(E) < 0.4] = low
+    masked[1] = low
+    masked[2, per:] = low
+    masked[3, :per], masked[3, per:] = -INF, low
+    masked[4, per + 1:] = -INF
+    masked[4, :per] = low
+    for ng, kg in ((1, 1), (8, 3), (4, 2)):
+        for k in (6, min(32, kg * E // ng - 2)):
+            check_route(masked, torch.float32, k, score=score, n_group=ng, topk_group=kg)
+    high = -low
+    for group in ([-INF, low, 0, low, -INF, 0, low, -INF], [low, -INF, low, low, 0, 0.1, -0.1, low],
+                  [low] * 8, [low, low / 2, low / 4, low, -INF, low / 2, low, low], [high, 0, high / 2, high, 0, 0, high, 0]):
+        bias = np.repeat(np.asarray(group, np.float64), per)
+        for some in (False, True):
+            if some:         # one ordinary expert in the masked groups too
+                bias[per // 2::per] = 0.25
+            for ng, kg in ((1, 1), (8, 3), (8, 5), (8, 7), (4, 2)):
+                for k in (6, min(32, kg * E // ng - 2)):
+                    check_route(l, torch.float32, k, bias, score=score, n_group=ng, topk_group=kg)
+        bias = np.where(rng.random(E) < 0.5, low, bias)
+        check_route(l, torch.float32, 6, bias, score=score, n_group=8, topk_group=3)
+
+
 def test_route_backward_same_expert_twice_masked_gradients_and_bad_index():
     rng = np.random.default_rng(9)
     l, k = rng.normal(size=(3, 16)).astype(np.float32), 3
