@@ -164,7 +164,7 @@ __device__ __forceinline__ T warp_sum(T v)
 // whole keys, in binary64 where there is a bias; where two groups at the border are, the token is done
 // again with whole keys throughout.  Both are rare (binary64 for every token: 65 us instead of 16 below).
 // Bound by latency and instruction issue: 8192 tokens of 256 experts in 8 groups with a bias take 16 us,
-// without groups and bias 10 us (their 8 MB of logits 1.3 us); one token 3.7 us.
+// without groups and bias 9 us (their 8 MB of logits 1.3 us); one token 3.5 us.
 // ------------------------------------------------------------------------------------------
 // Keys as unsigned integers of the same order, above 1.  0: not to be chosen (again); 1: masked.
 __device__ __forceinline__ uint32_t rank_of(float f)
@@ -307,16 +307,19 @@ __device__ __forceinline__ float pair_score(float a, float b) { return fminf(fma
 
 // The same choice from truncated keys, in about half the instructions: the low bits of a key's rank
 // hold its place in the lane (the lowest index the highest), so a lane's keys sort as plain integers
-// and the winner carries its index.  Ties of truncated keys go to the lower index.  Where two neighbours in
-// this order are not more than `near` apart, the k and all that are within `near` of the k-th are put in
-// order by their whole keys, one a lane.  *unsure is set where that is not enough: two groups at the
-// border within near_group of each other, or more than 32 candidates.
+// and the winner carries its index.  Ties of truncated keys go to the lower index.  Two keys p, q are near where
+// they are not more than fixed + rel max(|p|, |q|) apart: a bound that grows with the keys at hand, not with the
+// row's largest, because a mask of the type's lowest number is such a key (8192 tokens of 256 experts, a fifth
+// of the biases so masked: 15.9 us, 54 with the row's largest; 15.8 and 16.7 where none is).  Where two neighbours in this order are near,
+// the k and all that are near the k-th are put in order by their whole keys, one a lane.  (If a key is not near
+// the k-th, none behind it is: rel < 1.)  *unsure is set where that is not enough: a group that is kept and
+// one that is left out whose scores may be in the other order, or more than 32 candidates.
 // exact: truncation loses nothing (bf16 logits without a bias), so that ties are ties.
 // same(p, q): experts p and q have the same logit and bias.  exactly(e): the whole key of expert e, asked
 // by the whole warp.
 template <int NV, typename Same, typename Exactly>
 __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteShape& sh, bool pair, bool exact,
-                                           float near, float near_group, Same same, Exactly exactly, bool* unsure)
+                                           float fixed, float rel, Same same, Exactly exactly, bool* unsure)
 {
     constexpr uint32_t kPlace = NV - 1;   // NV is a power of two
     const int lane = threadIdx.x & 31, e0 = lane * NV, per = sh.per;
@@ -334,7 +337,11 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
     // Up to eight keys are sorted; longer lists cost more to sort than to search.
     if (NV <= 8 && (whole || !grouped)) sort_down<NV>(rank);
     if (grouped) {
-        float mine = -CUDART_INF_F;   // lane g: the score of group g
+        float mine = -CUDART_INF_F, off = 0.0f;   // lane g: the score of group g, and what it may be off by
+        // Twice what the two keys' errors, their truncation and the sum's rounding come to.
+        const auto off_by = [&](float a, float b) {
+            return fixed + rel * fabsf(a) + (pair && b > -CUDART_INF_F ? rel * fabsf(b) : 0.0f);
+        };
         if (whole) {
             float a = -CUDART_INF_F, b = -CUDART_INF_F;
             if (NV <= 8) {
@@ -347,6 +354,7 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
             for (int o = 1; o >> sh.shift == 0; o <<= 1)
                 merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
             mine = __shfl_sync(kFull, pair && b > -CUDART_INF_F ? pair_score(a, b) : a, (lane << sh.shift) & 31);
+            if (!exact) off = __shfl_sync(kFull, off_by(a, b), (lane << sh.shift) & 31);
         } else {
             for (int g = 0; g < sh.n_group; ++g) {
                 float a = -CUDART_INF_F, b = -CUDART_INF_F;
@@ -356,23 +364,27 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1)
                     merge_two(a, b, __shfl_xor_sync(kFull, a, o), __shfl_xor_sync(kFull, b, o));
-                if (lane == g) mine = pair && b > -CUDART_INF_F ? pair_score(a, b) : a;
+                if (lane == g) {
+                    mine = pair && b > -CUDART_INF_F ? pair_score(a, b) : a;
+                    off = off_by(a, b);
+                }
             }
         }
-        // The best groups one after another, and the first that is left out.
+        // The best groups one after another.
         uint32_t allowed = 0u, standing = lane < sh.n_group ? rank_of(mine) : 0u;
-        float in = 0.0f;
-        for (int j = 0; j <= sh.topk_group; ++j) {
+        for (int j = 0; j < sh.topk_group; ++j) {
             const uint32_t top = __reduce_max_sync(kFull, standing);
             const int g = __ffs(__ballot_sync(kFull, standing == top)) - 1;
-            const float score = key_of(top);
-            if (j == sh.topk_group) {
-                if (!exact && score > -CUDART_INF_F && !(in - score > near_group)) *unsure = true;
-            } else {
-                allowed |= 1u << g;
-                in = score;
-                if (lane == g) standing = 0u;
-            }
+            allowed |= 1u << g;
+            if (lane == g) standing = 0u;
+        }
+        if (!exact) {
+            // The least that one that is kept can have, and the most that one that is left out can have.  Masked
+            // groups are not off; if one is kept, all that are left out are masked.
+            const bool live = lane < sh.n_group && mine > -CUDART_INF_F, kept = (allowed >> lane) & 1u;
+            const uint32_t least = __reduce_min_sync(kFull, live && kept ? rank_of(mine - off) : 0xFFFFFFFFu);
+            const uint32_t most = __reduce_max_sync(kFull, live && !kept ? rank_of(mine + off) : 0u);
+            if (most >= least) *unsure = true;
         }
         // Experts of the other groups are out.  (A rank holds its place, wherever sorting took it.)
         if (whole) {
@@ -401,21 +413,22 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
     }
     // The k best one after another, and then all that are too near the k-th to be left out for certain.
     int chosen = 0, last_e = 0, n = 0;
-    float last = CUDART_INF_F, kth = CUDART_INF_F;
+    float last = 0.0f, kth = 0.0f;
     bool doubt = false;
     const int limit = min(32, sh.topk_group * per);
     for (; n < limit; ++n) {
         if (exact && n == sh.k) break;
         const uint32_t top = __reduce_max_sync(kFull, head & ~kPlace);
         const float value = value_of(top);
+        const auto near = [&](float above) { return !(above - value > fixed + rel * fmaxf(fabsf(above), fabsf(value))); };
         if (n >= sh.k) {
-            if (value == -CUDART_INF_F || kth - value > near) break;
+            if (value == -CUDART_INF_F || !near(kth)) break;
             doubt = true;
         }
         const int who = __ffs(__ballot_sync(kFull, (head & ~kPlace) == top)) - 1;   // the lowest lane: the lowest index
         const int e = __shfl_sync(kFull, e0 + (int)(kPlace - (head & kPlace)), who);
         if (!exact) {   // equal inputs have equal keys
-            if (n < sh.k && value > -CUDART_INF_F && !(last - value > near) && !same(last_e, e)) doubt = true;
+            if (n < sh.k && value > -CUDART_INF_F && n > 0 && near(last) && !same(last_e, e)) doubt = true;
             if (n == sh.k - 1) kth = value;
             last = value;
             last_e = e;
@@ -571,7 +584,8 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ lo
 
     // Scores.  e^x by __expf is off by (2 + 1.2 |x|) 2^-23 of itself, so sigmoid by less than 2^-22 in all
     // (s (1 - s) (2 + 1.2 |l|) < 0.65), and softmax, whose sum of up to 1024 terms adds 37 roundings, by
-    // less than 2^-18.  A key's own rounding is 2^-24 of it.  `near` is twice the sum of two such errors.
+    // less than 2^-18.  A key's own rounding is 2^-24 of it.  The bound of choose_fast
+    // is twice the sum of two such errors.
     float total = 0.0f, key[NV];
     if (SOFTMAX || bias) {
 #pragma unroll
@@ -583,10 +597,11 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ lo
         }
         if (SOFTMAX) total = warp_sum(total);
     }
-    // Truncation takes less than NV steps off a key, each at most 2^-23 of the largest key, or 2^-149.
+    // Truncation takes less than NV steps off a key, each at most 2^-23 of the key, or 2^-149.
     constexpr float kCut = NV * 0x1p-23f;
     const bool exact = !bias && sizeof(L) == 2;
-    float largest = 0.0f, near = 0.0f;
+    const float fixed = (bias ? (SOFTMAX ? 0x1p-16f : 0x1p-20f) : 0.0f) + 4 * NV * 0x1p-149f;
+    const float rel = (bias ? 0x1p-22f : 0.0f) + 2.0f * kCut;
     const float inv = SOFTMAX ? __fdividef(1.0f, total) : 1.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -594,11 +609,6 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ lo
             key[i] = r.l[i] > -CUDART_INF_F && r.b[i] > -CUDART_INF_F ? (SOFTMAX ? key[i] * inv : key[i]) + r.b[i] : -CUDART_INF_F;
         else
             key[i] = r.l[i];
-        if (key[i] > -CUDART_INF_F) largest = fmaxf(largest, fabsf(key[i]));
-    }
-    if (!exact) {
-        largest = warp_max(largest);
-        near = (bias ? (SOFTMAX ? 0x1p-16f : 0x1p-20f) + 0x1p-22f * largest : 0.0f) + 2.0f * kCut * largest + 4 * NV * 0x1p-149f;
     }
     bool unsure = false;
     const auto same = [&](int p, int q) {
@@ -618,7 +628,7 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ lo
         if (!(x > -CUDART_INF && x < CUDART_INF && b > -CUDART_INF && b < CUDART_INF)) return -CUDART_INF;
         return (SOFTMAX ? exp(x - (double)r.top) / sum : 1.0 / (1.0 + exp(-x))) + b;
     };
-    int chosen = choose_fast<NV>(key, sh, bias != nullptr, exact, near, 4.0f * near, same, exactly, &unsure);
+    int chosen = choose_fast<NV>(key, sh, bias != nullptr, exact, fixed, rel, same, exactly, &unsure);
     if (unsure) chosen = choose_exactly<L, NV, SOFTMAX>(row, bias, sh, wide);   // the same for the whole warp
 
     // Weights.  The renormalised ones divide scores by their sum, so scores that would underflow are
