@@ -313,7 +313,8 @@ __device__ __forceinline__ float pair_score(float a, float b) { return fminf(fma
 // of the biases so masked: 15.9 us, 54 with the row's largest; 15.8 and 16.7 where none is).  Where two neighbours in this order are near,
 // the k and all that are near the k-th are put in order by their whole keys, one a lane.  (If a key is not near
 // the k-th, none behind it is: rel < 1.)  *unsure is set where that is not enough: a group that is kept and
-// one that is left out whose scores may be in the other order, or more than 32 candidates.
+// one that is left out whose scores may be in the other order, or more than 32 candidates (with k = 32, one key
+// near the 32nd is enough).
 // exact: truncation loses nothing (bf16 logits without a bias), so that ties are ties.
 // same(p, q): experts p and q have the same logit and bias.  exactly(e): the whole key of expert e, asked
 // by the whole warp.
@@ -415,14 +416,17 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
     int chosen = 0, last_e = 0, n = 0;
     float last = 0.0f, kth = 0.0f;
     bool doubt = false;
-    const int limit = min(32, sh.topk_group * per);
-    for (; n < limit; ++n) {
-        if (exact && n == sh.k) break;
+    const int last_n = exact ? sh.k : sh.topk_group * per;   // all that can be chosen
+    for (; n < last_n; ++n) {
         const uint32_t top = __reduce_max_sync(kFull, head & ~kPlace);
         const float value = value_of(top);
         const auto near = [&](float above) { return !(above - value > fixed + rel * fmaxf(fabsf(above), fabsf(value))); };
         if (n >= sh.k) {
             if (value == -CUDART_INF_F || !near(kth)) break;
+            if (n == 32) {   // no lane is left for it
+                *unsure = true;
+                break;
+            }
             doubt = true;
         }
         const int who = __ffs(__ballot_sync(kFull, (head & ~kPlace) == top)) - 1;   // the lowest lane: the lowest index
@@ -452,7 +456,6 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
         }
     }
     if (doubt) {
-        if (n == 32 && limit < sh.topk_group * per) *unsure = true;   // perhaps not all of them
         // Lane i: candidate i's whole key, and how many come before it.
         const double whole_key = exactly(chosen);
         int before = 0;

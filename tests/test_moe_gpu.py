@@ -115,6 +115,46 @@ def test_route_orders_logits_one_step_apart(E, unit):
                 check_route(logits, torch.float32, 8, bias, score=score, n_group=n_group, topk_group=topk_group)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("k", [1, 8, 31, 32])
+@pytest.mark.parametrize("E", [48, 64, 128, 256, 600, 1024])
+def test_route_near_tie_at_the_last_place(E, k, score):
+    # k - 1 keys far above, two within a few fp32 steps of each other at places k and k + 1, the rest far below: the
+    # larger of the two is chosen, at the lower index or the higher.  The experts of the last of four groups are
+    # the lowest of all, so that the choice of three groups leaves the pair in.
+    rng = np.random.default_rng(E + k)
+    inside = rng.permutation(E // 4 * 3)
+    far, (lo, hi) = inside[:k - 1], np.sort(inside[k - 1:k + 1])
+    steps = np.repeat(np.arange(1, 8), 2)
+    logits = np.empty((14, E), np.float32)
+    logits[:] = -2.0 - rng.random((14, E))
+    logits[:, E // 4 * 3:] -= 8.0
+    logits[:, far] = 3.0 + 0.5 * rng.permuted(np.tile(np.arange(k - 1), (14, 1)), axis=1)
+    up = np.where(np.arange(14) % 2, hi, lo)
+    logits[:, lo] = logits[:, hi] = 1.0
+    logits[np.arange(14), up] = 1.0 + steps * 2.0 ** -23
+    groups = [dict(n_group=1, topk_group=1), dict(n_group=4, topk_group=3)]
+    for g in groups:
+        _, idx, _ = check_route(logits, torch.float32, k, score=score, **g)
+        assert (host(idx)[:, k - 1] == up).all()
+    # The same with a bias that sets the far keys apart: the pair's scores differ by less than fp32 holds.
+    bias = np.full(E, -2.0, np.float32)
+    bias[far], bias[[lo, hi]], bias[E // 4 * 3:] = 1.0 + 0.5 * np.arange(k - 1), -0.7, -9.0
+    for g in groups:
+        _, idx, _ = check_route(logits, torch.float32, k, bias, score=score, **g)
+        assert (host(idx)[:, k - 1] == up).all()
+    # Equal logits whose biases are one step apart, and exactly equal ones.
+    logits[:, [lo, hi]] = 1.0
+    for e in (lo, hi, None):
+        b = bias.copy()
+        if e is not None:
+            b[e] = np.nextafter(b[e], np.float32(0))
+        for dtype in (torch.float32, torch.bfloat16):
+            for g in groups:
+                _, idx, _ = check_route(logits, dtype, k, b, score=score, **g)
+                assert (host(idx)[:, k - 1] == (lo if e is None else e)).all()
+
+
 @pytest.mark.parametrize("E,n_group,topk_group", [(256, 8, 4), (256, 16, 5), (128, 4, 2), (384, 12, 4), (512, 8, 8)])
 def test_route_many_tokens(E, n_group, topk_group):
     # Enough tokens for every kind of near tie.
