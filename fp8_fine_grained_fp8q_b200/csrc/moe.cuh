@@ -164,7 +164,8 @@ __device__ __forceinline__ T warp_sum(T v)
 // whole keys, in binary64 where there is a bias; where two groups at the border are, the token is done
 // again with whole keys throughout.  Both are rare (binary64 for every token: 65 us instead of 16 below).
 // Bound by latency and instruction issue: 8192 tokens of 256 experts in 8 groups with a bias take 16 us,
-// without groups and bias 9 us (their 8 MB of logits 1.3 us); one token 3.5 us.
+// without groups and bias 8.2 us (their 8 MB of logits 1.3 us); one token 3.3 us.  Where all logits and biases are equal,
+// as in a router at its start, 20 and 12.5 us (51 and 33 where equal inputs counted as doubt).
 // ------------------------------------------------------------------------------------------
 // Keys as unsigned integers of the same order, above 1.  0: not to be chosen (again); 1: masked.
 __device__ __forceinline__ uint32_t rank_of(float f)
@@ -310,9 +311,9 @@ __device__ __forceinline__ float pair_score(float a, float b) { return fminf(fma
 // and the winner carries its index.  Ties of truncated keys go to the lower index.  Two keys p, q are near where
 // they are not more than fixed + rel max(|p|, |q|) apart: a bound that grows with the keys at hand, not with the
 // row's largest, because a mask of the type's lowest number is such a key (8192 tokens of 256 experts, a fifth
-// of the biases so masked: 15.9 us, 54 with the row's largest; 15.8 and 16.7 where none is).  Where two neighbours in this order are near,
-// the k and all that are near the k-th are put in order by their whole keys, one a lane.  (If a key is not near
-// the k-th, none behind it is: rel < 1.)  *unsure is set where that is not enough: a group that is kept and
+// of the biases so masked: 15.9 us, 54 with the row's largest; 15.8 and 16.7 where none is).  Where two neighbours in this order are near
+// and have not the same inputs, the k and all that are near the k-th are put in order by their whole keys, one a
+// lane.  (If a key is not near the k-th, none behind it is: rel < 1.)  *unsure is set where that is not enough: a group that is kept and
 // one that is left out whose scores may be in the other order, or more than 32 candidates (with k = 32, one key
 // near the 32nd is enough).
 // exact: truncation loses nothing (bf16 logits without a bias), so that ties are ties.
@@ -412,32 +413,10 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
 #pragma unroll
         for (int i = 1; i < NV; ++i) head = max(head, rank[i]);
     }
-    // The k best one after another, and then all that are too near the k-th to be left out for certain.
-    int chosen = 0, last_e = 0, n = 0;
-    float last = 0.0f, kth = 0.0f;
-    bool doubt = false;
-    const int last_n = exact ? sh.k : sh.topk_group * per;   // all that can be chosen
-    for (; n < last_n; ++n) {
-        const uint32_t top = __reduce_max_sync(kFull, head & ~kPlace);
-        const float value = value_of(top);
-        const auto near = [&](float above) { return !(above - value > fixed + rel * fmaxf(fabsf(above), fabsf(value))); };
-        if (n >= sh.k) {
-            if (value == -CUDART_INF_F || !near(kth)) break;
-            if (n == 32) {   // no lane is left for it
-                *unsure = true;
-                break;
-            }
-            doubt = true;
-        }
+    // The best one left, whose truncated rank is `top`, is taken out.
+    const auto take = [&](uint32_t top) {
         const int who = __ffs(__ballot_sync(kFull, (head & ~kPlace) == top)) - 1;   // the lowest lane: the lowest index
         const int e = __shfl_sync(kFull, e0 + (int)(kPlace - (head & kPlace)), who);
-        if (!exact) {   // equal inputs have equal keys
-            if (n < sh.k && value > -CUDART_INF_F && n > 0 && near(last) && !same(last_e, e)) doubt = true;
-            if (n == sh.k - 1) kth = value;
-            last = value;
-            last_e = e;
-        }
-        if (lane == n) chosen = e;
         if (NV <= 8) {
             if (lane == who) {
 #pragma unroll
@@ -453,6 +432,50 @@ __device__ __forceinline__ int choose_fast(const float (&key)[NV], const RouteSh
                 best = max(best, rank[i]);
             }
             head = best;
+        }
+        return e;
+    };
+    const auto near = [&](float above, float below) {
+        return !(above - below > fixed + rel * fmaxf(fabsf(above), fabsf(below)));
+    };
+    // The k best one after another.
+    int chosen = 0, last_e = 0, n = 0;
+    float last = 0.0f;
+    bool doubt = false;
+    for (; n < sh.k; ++n) {
+        const uint32_t top = __reduce_max_sync(kFull, head & ~kPlace);
+        const float value = value_of(top);
+        const int e = take(top);
+        if (!exact) {   // equal inputs have equal keys
+            if (value > -CUDART_INF_F && n > 0 && near(last, value) && !same(last_e, e)) doubt = true;
+            last = value;
+            last_e = e;
+        }
+        if (lane == n) chosen = e;
+    }
+    const float next = exact ? -CUDART_INF_F : value_of(__reduce_max_sync(kFull, head & ~kPlace));
+    if (next > -CUDART_INF_F && near(last, next)) {
+        // Equal inputs stand in the order of the index: no doubt about the border if all that are near the k-th have
+        // its inputs.  (Those before it have, unless there is doubt among them.)
+        bool differ = doubt;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const float v = value_of(rank[i]);
+            if (v > -CUDART_INF_F && near(last, v)) differ |= !same(last_e, e0 + (int)(kPlace - (rank[i] & kPlace)));
+        }
+        if (__any_sync(kFull, differ)) {
+            doubt = true;
+            for (;; ++n) {   // all that are too near the k-th to be left out for certain
+                const uint32_t top = __reduce_max_sync(kFull, head & ~kPlace);
+                const float value = value_of(top);
+                if (value == -CUDART_INF_F || !near(last, value)) break;
+                if (n == 32) {   // no lane is left for it
+                    *unsure = true;
+                    break;
+                }
+                const int e = take(top);
+                if (lane == n) chosen = e;
+            }
         }
     }
     if (doubt) {
@@ -548,12 +571,47 @@ __device__ __forceinline__ void load_route(RouteRow<L, NV>& r, const L* row, con
     r.top = warp_max(top);
 }
 
-// The choice from whole keys: the logits, or with a bias binary64 sums.
+// Whether all usable experts of the row have the same logit and the same bias, and (`pair`) as many of them count
+// for the score of every group that has any: one, or two.  Their keys, and those groups' scores, are then equal.
+template <typename L, int NV>
+__device__ __forceinline__ bool uniform_row(const RouteRow<L, NV>& r, const RouteShape& sh, bool pair)
+{
+    const int e0 = (threadIdx.x & 31) * NV;
+    float top_l = -CUDART_INF_F, low_l = CUDART_INF_F, top_b = -CUDART_INF_F, low_b = CUDART_INF_F;
+    bool masked = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (r.l[i] > -CUDART_INF_F && r.b[i] > -CUDART_INF_F) {
+            top_l = fmaxf(top_l, r.l[i]);
+            low_l = fminf(low_l, r.l[i]);
+            top_b = fmaxf(top_b, r.b[i]);
+            low_b = fminf(low_b, r.b[i]);
+        } else {
+            masked |= e0 + i < sh.E;
+        }
+    }
+    if (warp_max(top_l) != -warp_max(-low_l) || warp_max(top_b) != -warp_max(-low_b)) return false;
+    if (!pair || !__any_sync(kFull, masked)) return true;
+    int kinds = 0;   // 1: a group of one usable expert, 2: of more
+    for (int g = 0; g < sh.n_group; ++g) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (e0 + i >= g * sh.per && e0 + i < (g + 1) * sh.per && r.l[i] > -CUDART_INF_F && r.b[i] > -CUDART_INF_F) ++n;
+        n = warp_sum(n);
+        if (n > 0) kinds |= n > 1 ? 2 : 1;
+    }
+    return kinds != 3;
+}
+
+// The choice from whole keys: the logits, or with a bias binary64 sums.  `fast`: what choose_fast made of it, which
+// has the order of the index where nothing else orders the experts.
 template <typename L, int NV, bool SOFTMAX>
-__device__ __noinline__ int choose_exactly(const L* row, const float* bias, RouteShape sh, bool wide)
+__device__ __noinline__ int choose_exactly(const L* row, const float* bias, RouteShape sh, bool wide, int fast)
 {
     RouteRow<L, NV> r;
     load_route<L, NV>(r, row, bias, sh.E, wide);
+    if (uniform_row<L, NV>(r, sh, bias != nullptr && sh.n_group > sh.topk_group)) return fast;
     if (!bias) return choose<float, NV>(r.l, sh, false);
     double key[NV], total = 0.0;
 #pragma unroll
@@ -632,7 +690,7 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ lo
         return (SOFTMAX ? exp(x - (double)r.top) / sum : 1.0 / (1.0 + exp(-x))) + b;
     };
     int chosen = choose_fast<NV>(key, sh, bias != nullptr, exact, fixed, rel, same, exactly, &unsure);
-    if (unsure) chosen = choose_exactly<L, NV, SOFTMAX>(row, bias, sh, wide);   // the same for the whole warp
+    if (unsure) chosen = choose_exactly<L, NV, SOFTMAX>(row, bias, sh, wide, chosen);   // the same for the whole warp
 
     // Weights.  The renormalised ones divide scores by their sum, so scores that would underflow are
     // first scaled by exp(-m), m = min(largest chosen logit, 0): sigmoid(l) e^-m = e^(l-m) / (1 + e^l).

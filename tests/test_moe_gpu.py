@@ -155,6 +155,60 @@ def test_route_near_tie_at_the_last_place(E, k, score):
                 assert (host(idx)[:, k - 1] == (lo if e is None else e)).all()
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E", [64, 96, 256, 1024])
+def test_route_equal_inputs_around_a_near_tie(E, score):
+    # A smaller logit at the lowest index, one fp32 step below `copies` equal ones behind it, `inside` of which
+    # are among the first k by the index: all the places go to the equal ones, in the order of the index.
+    rng = np.random.default_rng(E)
+    k = 8
+    rows, want = [], []
+    for inside in (1, 2, 5, 8):
+        for copies in (inside, inside + 1, inside + 30, E - 1 - k):
+            at = np.sort(rng.permutation(E)[:copies + 1 + k - inside])
+            far, at = at[:k - inside], at[k - inside:]
+            l = np.full(E, -2.0, np.float32) - rng.random(E).astype(np.float32)
+            l[far], l[at[0]], l[at[1:]] = 3.0, 1.0, 1.0 + 2.0 ** -23
+            rows.append(l)
+            want.append(np.concatenate([far, at[1:]])[:k])
+    logits = np.stack(rows)
+    for bias in (None, np.full(E, -0.7, np.float32)):
+        _, idx, _ = check_route(logits, torch.float32, k, bias, score=score)
+        assert (host(idx) == want).all()
+        check_route(logits, torch.float32, k, bias, score=score, n_group=8, topk_group=5)
+        check_route(logits, torch.float32, 32, bias, score=score, n_group=8, topk_group=6)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,n_group", [(64, 8), (64, 32), (96, 8), (512, 8), (40, 20)])
+def test_route_one_input_everywhere_and_masks(E, n_group, dtype):
+    # Rows of one value, some of it masked, with groups that have two experts left, one or none.  The biases
+    # leave sums of a few 1e-9, of either sign: a group's two keys are then more than another's one, or less.
+    rng = np.random.default_rng(E + n_group)
+    per = E // n_group
+    for x in (0.0, 1.0, -0.375, 2.5, -40.0):
+        l = np.full((12, E), x, np.float32)
+        l[1, rng.random(E) < 0.5] = -INF
+        l[2, ::per] = -INF
+        l[3, per:] = -INF
+        l[4, :-per] = -INF
+        l[5] = -INF
+        l[6, rng.random(E) < 0.9] = -INF
+        for g in range(n_group):                 # two, one or no expert left
+            left = rng.permutation(per)[:(7, 2, 1, 0)[g % 4]]
+            l[7 + g % 3, g * per:(g + 1) * per] = -INF
+            l[7 + g % 3, g * per + left] = x
+            l[11, g * per:(g + 1) * per] = -INF
+            l[11, g * per + left] = x
+        near = np.float32(_moe.sigmoid(np.float64(x)))
+        for score in ("sigmoid", "softmax"):
+            for kg in (n_group // 2, n_group - 1):
+                for k in (1, min(8, kg * per), min(32, kg * per)):
+                    for b in (None, 0.0, 0.3, -near, -np.nextafter(near, np.float32(1)), -np.nextafter(near, np.float32(0))):
+                        check_route(l, dtype, k, None if b is None else np.full(E, b, np.float32), score=score,
+                                    n_group=n_group, topk_group=kg)
+
+
 @pytest.mark.parametrize("E,n_group,topk_group", [(256, 8, 4), (256, 16, 5), (128, 4, 2), (384, 12, 4), (512, 8, 8)])
 def test_route_many_tokens(E, n_group, topk_group):
     # Enough tokens for every kind of near tie.
