@@ -358,11 +358,14 @@ enum { FP8Q_SCORE_SIGMOID = 0, FP8Q_SCORE_SOFTMAX = 1 };
  *   score s = sigmoid(l), or softmax(l) over the token's experts;
  *   key = s + bias, or without a bias the logit itself (the order of the scores);
  *   the experts form n_group groups of E / n_group consecutive ones; a group's score is the sum of
- *   its two largest keys (without a bias: its largest); the topk_group best groups are kept, and
- *   the k best experts in them are chosen, in descending order.  Equal keys go to the lower index.
+ *   its two largest keys (without a bias, or with one unmasked expert left: its largest); the
+ *   topk_group best groups are kept, and the k best experts in them are chosen, in descending order.
+ *   Equal keys go to the lower index.
  *   w_j = scale s_j / (sum of the chosen s) with renormalize, scale s_j without.  The bias never
  *   enters w.
- * The order is that of the keys in binary64, whatever the logits' type; w is rounded to fp32 once.
+ * The order is that of the keys in binary64, whatever the logits' type.  w is formed in fp32, to a
+ * relative error below (64 + d) 2^-24, d the distance of its logit from the largest chosen one (from
+ * the row's largest for softmax without renormalize), or below (1 + |scale|) 2^-147.
  * A logit or bias of -inf masks its expert: it is chosen only where fewer than k unmasked experts are
  * left in the kept groups, lowest index first, with weight 0.  A NaN or +inf masks the expert too,
  * and makes all weights of the row NaN.  n_group <= 32, and E must be a multiple of it; scale is
@@ -375,7 +378,7 @@ FP8Q_API int fp8q_moe_route(const void* logits, int logits_type, const float* bi
 /*
  * Gradient of the weights' loss with respect to the logits: dw [T, k], with w and idx as
  * fp8q_moe_route returned them -> dlogits [T, E] in the logits' type, fully written.  The choice
- * itself and the bias have no gradient.  A slot of weight 0 takes no part.  An expert outside [0, E)
+ * itself and the bias have no gradient.  All fp32.  A slot of weight 0 takes no part.  An expert outside [0, E)
  * is left out and latches FP8Q_DEV_BAD_INDEX.
  */
 FP8Q_API int fp8q_moe_route_backward(const float* dw, const float* w, const int32_t* idx, const void* logits,
@@ -412,7 +415,7 @@ FP8Q_API int fp8q_moe_dispatch(const uint16_t* x, const int32_t* offsets, const 
  * Combine: out[t] = add[t] + sum over j of weights[t, j] y[rows[t, j]], summed in fp32 in the order of
  * j and rounded to bf16 once.  y : [M, C], add : [T, C] or NULL, out : [T, C], all bf16;
  * weights : [T, k] fp32, or NULL for ones.  The row of a weight that is 0 is not read (an infinity
- * there does no harm).  A row out of range is left out and latches FP8Q_DEV_BAD_INDEX.  C % 8 == 0.
+ * there does no harm).  Another row out of range is left out and latches FP8Q_DEV_BAD_INDEX.  C % 8 == 0.
  */
 FP8Q_API int fp8q_moe_combine(const uint16_t* y, const int32_t* rows, const float* weights_or_null,
                               const uint16_t* add_or_null, int64_t T, int32_t k, int64_t C, uint16_t* out,
@@ -429,6 +432,8 @@ FP8Q_API int fp8q_moe_combine_dweight(const uint16_t* dout, const uint16_t* y, c
  *   q  : [M, I] codes,   s  : [I/128, M]     a, quantised 1x128 from fp32
  *   hq : [M, 2 I] codes, hs : [2 I/128, M]   (both or neither NULL) the checkpoint: h itself, as
  *        fp8q_act_1x128(h), half the bytes of h
+ * sigmoid(g) is the hardware's approximate 2^x and reciprocal in fp32, off by less than
+ * (8 + 1.5 |g|) 2^-24 of itself, and 0 where it is below 2^-126 (g < -87.3); the products are fp32.
  * I % 128 == 0; any M.  A NaN in h gives NaN codes; a group holding an infinity dequantises to NaN.
  */
 FP8Q_API int fp8q_swiglu_quant(const uint16_t* h, int64_t M, int64_t I, uint8_t* q, float* s, uint8_t* hq_or_null,
@@ -436,7 +441,8 @@ FP8Q_API int fp8q_swiglu_quant(const uint16_t* h, int64_t M, int64_t I, uint8_t*
 
 /*
  * SwiGLU backward from the checkpoint: with g, u = the dequantised halves of (hq, hs), r = sigmoid(g),
- *   dh = [ da u r (1 + g (1 - r)),  da g r ],   a = g r u   (all fp32, quantised from there)
+ *   dh = [ da u r (1 + g (1 - r)),  da g r ],   a = g r u   (all fp32, r as fp8q_swiglu_quant's;
+ *   quantised from there)
  *   da : [M, I] bf16
  *   q  : [M, 2 I], s  : [2 I/128, M]          dh, 1x128: the operand of Dgrad
  *   qt : [2 I, Kcap], st : [Kcap/128, 2 I]    dh, ragged 128x1: the operand of the first GEMM's Wgrad

@@ -233,6 +233,31 @@ def test_route_many_tokens(E, n_group, topk_group):
                 assert torch.equal(idx.long(), want)
 
 
+@pytest.mark.parametrize("E,k", [(8, 8), (64, 32), (256, 8), (1024, 32)])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("spread", [1.0, 6.0, 40.0])
+def test_route_weights_to_the_error_that_is_stated(spread, score, renorm, E, k):
+    # In units of U32.  One score: an exponential of 2 steps (4) and of a difference d rounded once (d), one more
+    # exponential (2, being at most half of its sum), a sum and a quotient: 8 + d, and with the scale 9 + d.
+    # Renormalised, the sum of k of them is off by their mean of that, weighted with the scores (sum of p d < 2 for at
+    # most 32), and by 5 additions, and a quotient and the scale add 2: 25 + d.  softmax as it is: the sum of E fast
+    # exponentials is off by (2 + 1.2 d) 2 + d each, again weighted (sum of p d < 4.5 for at most 1024: 19.3), and by
+    # 37 additions; with the chosen one's 4 + d, a quotient and the scale 62.3 + d.  All are below the header's 64 + d.
+    # Below 2^-126 the exponential is off by 2 steps of 2^-149 and the quotient by half of one, times the scale.
+    rng = np.random.default_rng(E + k)
+    l = (spread * rng.normal(size=(200, E))).astype(np.float32)
+    idx, w = ops.moe_route(f32_dev(l), k, score=score, renormalize=renorm, scale=2.5)
+    ok()
+    ref_idx, ref = _moe.route(l, k, score=score, renormalize=renorm, scale=2.5)
+    assert np.array_equal(host(idx), ref_idx)
+    x = np.take_along_axis(l.astype(np.float64), ref_idx, 1)
+    top = np.minimum(x[:, :1], 0.0) if score == "sigmoid" else x[:, :1]      # idx is in descending order
+    d = np.maximum(top - x, 0.0)
+    steps = 25 + d if renorm else 9 + np.zeros_like(d) if score == "sigmoid" else 62.3 + d
+    assert (np.abs(host(w) - ref) <= steps * (1 + ELEM) * U32 * ref + 3.5 * 2.0 ** -147).all()
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_route_ties_go_to_the_lower_index(dtype):
     T, E = 5, 96
