@@ -465,6 +465,36 @@ def test_dispatch_is_the_quantisers_of_the_gathered_rows(T, k, E, C, weighted):
 
 
 @pytest.mark.parametrize("weighted", [False, True])
+def test_dispatch_many_tiles_a_cta(weighted):
+    # 300 experts of 0 to some 200 rows, 9 channel blocks: every CTA of the 128x1 form walks over several items of
+    # one to four blocks, in groups of more than 64 rows and of fewer.
+    T, k, E, C = 3001, 4, 300, 1152
+    rng = np.random.default_rng(5)
+    popular = np.exp(1.5 * rng.normal(size=E))
+    idx = np.argsort(-(np.log(popular) + rng.gumbel(size=(T, E))), axis=1)[:, :k].astype(np.int32)
+    off, slots, rows = _moe.plan(idx, E)
+    sizes = np.diff(off) % 128
+    assert ((sizes > 0) & (sizes <= 64)).sum() > 50 and (sizes > 64).sum() > 20
+    bits = synth.activations_channel_outliers(T, C, seed=2)
+    v = synth.bf16_bits_to_f32(bits)[slots // k]
+    w = None
+    if weighted:
+        w = (rng.random((T, k)) - 0.3).astype(np.float32)
+        v = (v * w.reshape(-1)[slots][:, None]).astype(np.float32)
+        w = f32_dev(w)
+    q, s, qt, st = dispatch(bits, ops.MoePlan(i32(off), i32(slots), i32(rows)), w)
+    ok()
+    for got, want in zip((q, s), _moe.quant_rows(v)):
+        same_bits(got, want, "rows")
+    wqt, wst = _moe.quant_cols(v, off)
+    K = wqt.shape[1]
+    assert K // 128 * 3 > 2 * 3 * 148
+    same_bits(qt[:, :K], wqt, "transposed codes")
+    same_bits(st[:K // 128], wst, "transposed scales")
+    assert bool((qt[:, K:] == 0xA5).all()) and bool(torch.isnan(st[K // 128:]).all()), "the tail was written"
+
+
+@pytest.mark.parametrize("weighted", [False, True])
 def test_dispatch_nan_and_infinity_show(weighted):
     x = np.zeros((3, 128), np.float32)
     x[0, 3], x[0, 4], x[0, 100] = NAN, 2.0, -NAN
@@ -651,6 +681,37 @@ def test_swiglu_backward_from_the_checkpoint(counts, I):
         assert (qt[:, K:] == 0xA5).all() and np.isnan(st[K // 128:]).all(), "the tail was written"
         padding = pad(np.ones((M, 1)))[0] == 0
         assert not qt[:, :K][:, padding].any(), "padding must hold zero codes"
+
+
+def test_swiglu_backward_many_tiles_a_cta():
+    # More than four tiles a CTA, groups of more than 64 rows and of fewer one after another.
+    rng = np.random.default_rng(7)
+    counts = rng.integers(0, 200, size=60)
+    counts[[3, 17, 18]] = 0, 64, 65
+    off, I = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32), 1152
+    M = int(off[-1])
+    assert sum(-(-n // 128) for n in counts) * (I // 128) > 4 * 148
+    da, hq, hs = swiglu_problem(M, I, seed=8)
+    args = bf16_dev(da), u8_dev(hq), f32_dev(hs)
+    q, s, qt, st, aqt, ast = got = ops.swiglu_backward_quant(*args, offsets=i32(off))
+    again = ops.swiglu_backward_quant(*args, offsets=i32(off))
+    ok()
+    h = (oracle.e4m3_decode(hq.reshape(-1)).reshape(hq.shape) * np.repeat(hs.T, 128, axis=1)).astype(np.float32)
+    (dg, du, a), (eg, eu, ea) = _moe.swiglu_backward(synth.bf16_bits_to_f32(da).astype(np.float64),
+                                                     h[:, :I].astype(np.float64), h[:, I:].astype(np.float64))
+    dh, eh = np.concatenate([dg, du], 1), np.concatenate([eg, eu], 1)
+    _moe.check_quantised(host(q), host(s), dh, eh, what="dh")
+    padding = _moe.padded_rows(np.ones((M, 1)), off)[:, 0] == 0
+    K = padding.size
+    for codes, scales, v, e, what in ((qt, st, dh, eh, "dh, transposed"), (aqt, ast, a, ea, "a, transposed")):
+        codes, scales = np.ascontiguousarray(host(codes)[:, :K]), np.ascontiguousarray(host(scales)[:K // 128])
+        _moe.check_quantised(codes, scales, np.ascontiguousarray(_moe.padded_rows(v, off).T),
+                             np.ascontiguousarray(_moe.padded_rows(e, off).T), what=what)
+        assert not codes[:, padding].any(), "padding must hold zero codes"
+    for x, y, rows in zip(got, again, (True, True, False, False, False, False)):
+        if not rows:                # what lies behind the last group is not written
+            x, y = (x[:, :K], y[:, :K]) if x.dtype == torch.uint8 else (x[:K // 128], y[:K // 128])
+        assert torch.equal(x, y)
 
 
 def test_swiglu_backward_bad_offsets_write_nothing():
