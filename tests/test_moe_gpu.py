@@ -912,6 +912,23 @@ def test_two_layers_on_two_streams_at_once():
                 assert torch.equal(v, g[name]), name
 
 
+def test_the_public_ways_to_device_and_stream_do_too(monkeypatch):
+    layer = Layer(T=60, seed=15)
+    want = layer.step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert ops._stream_now(0) == ops._public_stream(0) == side.cuda_stream
+    monkeypatch.setattr(ops, "_device_now", torch.cuda.current_device)
+    monkeypatch.setattr(ops, "_stream_now", ops._public_stream)
+    with torch.cuda.stream(side):
+        got = layer.step()
+    side.synchronize()
+    ok()
+    for name, v in want.items():
+        assert torch.equal(v, got[name]), name
+
+
 FIRST_USE = """
 import torch
 from fp8_fine_grained_fp8q_b200 import ops
