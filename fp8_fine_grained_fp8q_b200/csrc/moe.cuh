@@ -163,7 +163,8 @@ __device__ __forceinline__ T warp_sum(T v)
 // neighbours in the order found that way are nearer than the bound, the candidates are put in order by
 // whole keys, in binary64 where there is a bias; where two groups at the border are, the token is done
 // again with whole keys throughout.  Both are rare (binary64 for every token: 65 us instead of 16 below).
-// Bound by latency and instruction issue: 8192 tokens of 256 experts in 8 groups with a bias take 16 us,
+// Bound by instruction issue while the SMs are busy (0.71 of the slots; the ALU 0.63), and by the latency of one
+// token's rounds at either end of the launch: 8192 tokens of 256 experts in 8 groups with a bias take 16 us,
 // without groups and bias 8.2 us (their 8 MB of logits 1.3 us); one token 3.3 us.  Where all logits and biases are equal,
 // as in a router at its start, 20 and 12.5 us (51 and 33 where equal inputs counted as doubt).
 // ------------------------------------------------------------------------------------------
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const L* __restrict__ lo
     int chosen = choose_fast<NV>(key, sh, bias != nullptr, exact, fixed, rel, same, exactly, &unsure);
     if (unsure) chosen = choose_exactly<L, NV, SOFTMAX>(row, bias, sh, wide, chosen);   // the same for the whole warp
 
-    // Weights.  The renormalised ones divide scores by their sum, so scores that would underflow are
+    // Weights, in fp32: only the order needs more.  The renormalised ones divide scores by their sum, so scores that would underflow are
     // first scaled by exp(-m), m = min(largest chosen logit, 0): sigmoid(l) e^-m = e^(l-m) / (1 + e^l).
     bool usable = false;
     float x = -CUDART_INF_F;
@@ -1563,8 +1564,8 @@ __global__ void __launch_bounds__(256) moe_combine_dweight_kernel(const uint16_t
 // Bound by HBM: 65536 x 2048 with the checkpoint takes 158 us, 6.0 TB/s (the two MUFU operations an
 // element alone would take 60 us).  Two CTAs an SM with 110 registers; three with 80 spill: 176 us.
 // ------------------------------------------------------------------------------------------
-// sigmoid of two values by ex2 and a fast reciprocal: with the rounding of x log2 e, a relative error below
-// (4 + 1.5 |x|) 2^-24 and a few steps of the two functions; beyond |x| = 88 the result is 0 or 1.
+// sigmoid of two values by ex2 and a fast reciprocal.  In units of 2^-24 of the result: 1.25 |x| from x log2 e and its
+// rounding, 3 and 2 from the two functions, 1 from the sum: below 8 + 1.5 |x|.  Results below 2^-126 are 0.
 __device__ __forceinline__ float2 sigmoid2(float2 x)
 {
     const float2 t = mul2(x, both(-1.442695041f));   // -log2 e
@@ -1672,8 +1673,10 @@ __global__ void __launch_bounds__(256, 2) swiglu_quant_kernel(const uint16_t* __
 // take 86 us instead of 101): the 96 values, three an element, are computed once and stay in
 // registers until both quantisations are done.  Columns lie inside a warp, so their scales need shuffles
 // only and their codes leave as whole lines; rows meet in shared memory.
-// The values fill the register file with one CTA an SM.  Bound by instruction issue (0.58 of the slots)
-// and the latencies between three barriers: 65536 x 2048 in 645 groups take 300 us, 4.1 TB/s.
+// The values fill the register file with one CTA an SM, four warps a scheduler, and what bounds it is that these
+// are too few: 0.57 of the issue slots and no pipe above 0.42 (ALU; FMA 0.34, MUFU and conversions 0.23) in use, and of
+// the 7.0 cycles between two instructions of a warp 0.9 at barriers, 0.9 in fixed latencies, 0.8 behind another
+// warp in a pipe, 0.75 for shared memory and MUFU results.  65536 x 2048 in 645 groups take 300 us, 4.1 TB/s.
 // ------------------------------------------------------------------------------------------
 constexpr int kBackThreads = 512;
 constexpr int kBackStage = 128 * 256 + 2 * 128 * 128 + 2 * 128 * 4;   // da, the codes of g and u, their scales
